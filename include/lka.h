@@ -72,7 +72,7 @@ typedef enum {
                                  was saturated (the output is finite but not accurate); see (b) */
 } lka_status_t;
 
-typedef enum { LKA_BF16 = 0, LKA_FP32 = 1 } lka_dtype_t;
+typedef enum { LKA_BF16 = 0, LKA_FP32 = 1, LKA_E4M3 = 2 } lka_dtype_t;  /* LKA_E4M3: caches of gqa_evict only */
 
 /* ------------------------------------------------------------------------ */
 /* (a) GQA attention  [GQA "How GQA works"]                                 */
@@ -328,6 +328,139 @@ LKA_API lka_status_t gta_shared_score_attn_paged(const void *q_g, const void *k_
 LKA_API lka_status_t latent_expand_cache(const void *latent, const void *w_uk, const void *w_uv, int B, int Lmax, int g,
                                  int d_h, int r_kv, int d_r, void *kc, void *vc, void *kr, lka_dtype_t dtype,
                                  void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* (e) Cache operators around the attention calls                           */
+/*  Rotary positions.  Pair i of a head (0 <= i < d_rot/2) at position p is  */
+/*  turned by p * inv_freq[i] and scaled by `amplitude`; values from d_rot   */
+/*  on pass through.  interleaved == 0 pairs values (i, i + d_rot/2),        */
+/*  otherwise (2i, 2i + 1).  inv_freq [d_rot/2] is fp64 (device), radians    */
+/*  per token: scaled positions for long contexts are a choice of inv_freq   */
+/*  and amplitude.  Angles are formed in fp64, the rotation in fp32, results */
+/*  are rounded once.  d_rot even, at most 512.                              */
+/* ------------------------------------------------------------------------ */
+/* x [B,h,s,d] (bf16 or fp32) -> out, both through strides in elements {batch, head, token} (host arrays; the last
+ * dimension is contiguous); positions [B,s] int32.  out may be x with the same strides.  backward != 0 applies the
+ * transpose (the gradient of x given the gradient of out).  No workspace. */
+LKA_API lka_status_t rope_apply(const void *x, const int64_t *x_strides, const int32_t *positions,
+                                const double *inv_freq, void *out, const int64_t *out_strides, int B, int h, int s,
+                                int d, int d_rot, int interleaved, int backward, float amplitude, lka_dtype_t dtype,
+                                void *stream);
+
+/* Rotation of a step's queries and keys and the write of its keys and values into the cache.
+ *   q [B,h_q,s_q,d_h], k, v [B,h_kv,s_q,d_h] through strides (host array of 9: q, k, v x batch, head, token)
+ *   q_out [B,h_q,s_q,d_h] contiguous; caches as in (a), (a') and (a'')
+ * cache_lens[b] = L_b counts the cached tokens INCLUDING the s_q new ones: token t goes to row L_b - s_q + t.
+ * positions [B,s_q] int32 or NULL (then the row is the position; a cache that has evicted keys passes the true
+ * positions).  Tokens with L_b - s_q + t < 0 are padding: nothing is written for them and their q_out rows are 0
+ * (L_b == 0 skips the sequence).  L_b outside [0, Lmax] is treated the same and raises LKA_ERR_BAD_LENGTH; a page
+ * outside the pool is not written and raises LKA_ERR_BAD_PAGE.  Every other cache row keeps its contents.
+ * The workspace is only the status header (256 bytes).  e4m3 caches hold value / scale, rounded to nearest even
+ * and saturated at 448. */
+LKA_API lka_status_t gqa_rope_append(const void *q, const void *k, const void *v, const int64_t *strides,
+                                     const int32_t *cache_lens, const int32_t *positions, const double *inv_freq,
+                                     void *q_out, void *k_cache, void *v_cache, int B, int h_q, int h_kv, int s_q,
+                                     int d_h, int d_rot, int Lmax, int interleaved, float amplitude,
+                                     lka_dtype_t dtype, void *ws, size_t ws_bytes, void *stream);
+LKA_API lka_status_t gqa_rope_append_paged(const void *q, const void *k, const void *v, const int64_t *strides,
+                                           const int32_t *block_table, const int32_t *cache_lens,
+                                           const int32_t *positions, const double *inv_freq, void *q_out,
+                                           void *k_pages, void *v_pages, int B, int h_q, int h_kv, int s_q, int d_h,
+                                           int d_rot, int page_size, int max_pages, int num_pages, int interleaved,
+                                           float amplitude, lka_dtype_t dtype, void *ws, size_t ws_bytes,
+                                           void *stream);
+LKA_API lka_status_t gqa_rope_append_fp8kv(const void *q, const void *k, const void *v, const int64_t *strides,
+                                           const float *k_scale, const float *v_scale, const int32_t *cache_lens,
+                                           const int32_t *positions, const double *inv_freq, void *q_out,
+                                           void *k_cache, void *v_cache, int B, int h_q, int h_kv, int s_q, int d_h,
+                                           int d_rot, int Lmax, int interleaved, float amplitude, void *ws,
+                                           size_t ws_bytes, void *stream);
+/* The same for the latent cache of (b): q_r [B,h_q,s_q,d_r] and k_r [B,1,s_q,d_r] are rotated (all d_r values),
+ * c_kv [B,1,s_q,r_kv] is copied; the cache row is [c_kv ; k_r].  strides: those of q_r, k_r, c_kv in this order.
+ * Only the rotary queries pass through here (q_out [B,h_q,s_q,d_r]). */
+LKA_API lka_status_t latent_rope_append(const void *q_r, const void *c_kv, const void *k_r, const int64_t *strides,
+                                        const int32_t *cache_lens, const int32_t *positions, const double *inv_freq,
+                                        void *q_out, void *latent, int B, int h_q, int s_q, int r_kv, int d_r,
+                                        int Lmax, int interleaved, float amplitude, lka_dtype_t dtype, void *ws,
+                                        size_t ws_bytes, void *stream);
+LKA_API lka_status_t latent_rope_append_paged(const void *q_r, const void *c_kv, const void *k_r,
+                                              const int64_t *strides, const int32_t *block_table,
+                                              const int32_t *cache_lens, const int32_t *positions,
+                                              const double *inv_freq, void *q_out, void *latent_pages, int B, int h_q,
+                                              int s_q, int r_kv, int d_r, int page_size, int max_pages, int num_pages,
+                                              int interleaved, float amplitude, lka_dtype_t dtype, void *ws,
+                                              size_t ws_bytes, void *stream);
+LKA_API lka_status_t latent_rope_append_fp8kv(const void *q_r, const void *c_kv, const void *k_r,
+                                              const int64_t *strides, const float *kv_scale,
+                                              const int32_t *cache_lens, const int32_t *positions,
+                                              const double *inv_freq, void *q_out, void *latent, int B, int h_q,
+                                              int s_q, int r_kv, int d_r, int Lmax, int interleaved, float amplitude,
+                                              void *ws, size_t ws_bytes, void *stream);
+
+/* GQA attention of a batch that shares one cached prefix.  Every query sees all P prefix keys, then its own
+ * sequence's suffix with the rules of (a): cache_lens[b] counts the SUFFIX tokens including the s_q new ones
+ * (1 <= L_b <= Lmax, L_b >= s_q when causal; clamped and reported otherwise).
+ *   q, out [B,h_q,s_q,d_h]   k_prefix, v_prefix [h_kv,Lp,d_h]   k, v [B,h_kv,Lmax,d_h]   lse [B,h_q,s_q] or NULL
+ *   prefix_len: device int32 [1] with 0 <= P <= Lp (clamped and reported), or NULL for P = Lp; Lp may be 0.
+ * bf16 (d_h in {64, 128, 256}) or fp32 (d_h in {64, 128}).  The prefix is read once for the query rows of all
+ * sequences together; softmax statistics and partial outputs are fp32.
+ * Paged: one pool for prefix and suffixes; the prefix's pages are prefix_table [max_prefix_pages], a suffix starts
+ * at row 0 of its own first page block_table[b][0].  Other arguments as in (a'). */
+LKA_API size_t gqa_attn_shared_prefix_workspace_size(int B, int h_q, int h_kv, int s_q, int d_h, int Lp, int Lmax,
+                                                     lka_dtype_t dtype);
+LKA_API lka_status_t gqa_attn_shared_prefix(const void *q, const void *k_prefix, const void *v_prefix,
+                                            const int32_t *prefix_len, const void *k, const void *v,
+                                            const int32_t *cache_lens, void *out, float *lse, int B, int h_q,
+                                            int h_kv, int s_q, int d_h, int Lp, int Lmax, int causal, float scale,
+                                            lka_dtype_t dtype, void *ws, size_t ws_bytes, void *stream);
+LKA_API size_t gqa_attn_shared_prefix_paged_workspace_size(int B, int h_q, int h_kv, int s_q, int d_h, int page_size,
+                                                           int max_prefix_pages, int max_pages, lka_dtype_t dtype);
+LKA_API lka_status_t gqa_attn_shared_prefix_paged(const void *q, const void *k_pages, const void *v_pages,
+                                                  const int32_t *prefix_table, const int32_t *prefix_len,
+                                                  const int32_t *block_table, const int32_t *cache_lens, void *out,
+                                                  float *lse, int B, int h_q, int h_kv, int s_q, int d_h,
+                                                  int page_size, int max_prefix_pages, int max_pages, int num_pages,
+                                                  int causal, float scale, lka_dtype_t dtype, void *ws,
+                                                  size_t ws_bytes, void *stream);
+
+/* The attention weight every cached key received:
+ *   weights[b,h,j] (+)= sum over the heads of KV head h's group and the queries t that see key j of
+ *                       exp(scale <q, k_j> - lse)
+ *   q [B,h_q,s_q,d_h]  k [B,h_kv,Lmax,d_h] (or pages)  lse [B,h_q,s_q] as gqa_attn returned it
+ *   weights [B,h_kv,Lmax] fp32: accumulate == 0 writes them (0 at j >= L_b), otherwise adds (j >= L_b untouched).
+ * Rows with lse = -inf (no visible key) add nothing.  Deterministic (no atomics).  Types, lengths, masks and pages
+ * as in (a) and (a').  The workspace is only the status header (256 bytes). */
+LKA_API lka_status_t gqa_key_weights(const void *q, const void *k, const float *lse, const int32_t *cache_lens,
+                                     float *weights, int B, int h_q, int h_kv, int s_q, int d_h, int Lmax, int causal,
+                                     int accumulate, float scale, lka_dtype_t dtype, void *ws, size_t ws_bytes,
+                                     void *stream);
+LKA_API lka_status_t gqa_key_weights_paged(const void *q, const void *k_pages, const float *lse,
+                                           const int32_t *block_table, const int32_t *cache_lens, float *weights,
+                                           int B, int h_q, int h_kv, int s_q, int d_h, int page_size, int max_pages,
+                                           int num_pages, int causal, int accumulate, float scale, lka_dtype_t dtype,
+                                           void *ws, size_t ws_bytes, void *stream);
+
+/* Cuts a cache to at most `budget` keys per KV head.  With L_b > budget keys, the first `sinks` and the last
+ * `recent` keys stay (sinks first, where the budget is smaller than both), and of the others those with the largest
+ * weights (ties: the lowest position; NaN counts as less than every number).  The kept rows of k, v and weights move
+ * to rows 0 .. n-1, n = min(L_b, budget), in the order of their positions; weights_out is 0 from n on, k_out and
+ * v_out rows from n on keep their contents.
+ *   k, v [B,h_kv,Lmax,d_h]  weights [B,h_kv,Lmax] -> k_out, v_out [B,h_kv,Lout,d_h]  weights_out [B,h_kv,Lout]
+ *   new_lens [B] = n (not the array cache_lens)   kept [B,h_kv,budget] the positions, ascending, -1 behind them
+ * Outputs are other buffers than the inputs, or all three the same buffers (in place, Lout == Lmax).
+ * 0 <= L_b <= Lmax (clamped and reported).  dtype: bf16, fp32 or LKA_E4M3 with d_h values of a multiple of 16 bytes.
+ * Paged: in place, rows addressed through block_table; pages the new length no longer reaches are free; the pages
+ * of a sequence are its own.  A destination page outside the pool is not written (LKA_ERR_BAD_PAGE).
+ * The workspace is only the status header (256 bytes).  Positions of later tokens must come from the caller
+ * (gqa_rope_append's `positions`), since cache_lens no longer counts the tokens seen. */
+LKA_API lka_status_t gqa_evict(const void *k, const void *v, const float *weights, const int32_t *cache_lens,
+                               void *k_out, void *v_out, float *weights_out, int32_t *new_lens, int32_t *kept, int B,
+                               int h_kv, int d_h, int Lmax, int Lout, int budget, int sinks, int recent,
+                               lka_dtype_t dtype, void *ws, size_t ws_bytes, void *stream);
+LKA_API lka_status_t gqa_evict_paged(void *k_pages, void *v_pages, float *weights, const int32_t *block_table,
+                                     const int32_t *cache_lens, int32_t *new_lens, int32_t *kept, int B, int h_kv,
+                                     int d_h, int page_size, int max_pages, int num_pages, int budget, int sinks,
+                                     int recent, lka_dtype_t dtype, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Helpers                                                                  */

@@ -19,6 +19,14 @@ Entry points (same names as the C ABI):
   gta_shared_score_attn    GTA shared score per group    (GTA article, grouped shared attention matrix)
   gta_shared_score_attn_paged  the same over paged K/V pools (chunked prefill against a paged cache)
   latent_expand_cache      one-time latent -> expanded cache conversion (GQLA paper, sec. 3.1)
+
+Operators around the attention calls (cache_ops.py):
+  rope, rope_inv_freq      rotary positions and their gradient; frequencies, scaled for long contexts
+  gqa_rope_append / _paged / _fp8kv, latent_rope_append / _paged / _fp8kv
+                           rotation of a step's queries and keys fused with the write into the cache
+  gqa_attn_shared_prefix / _paged   GQA attention of a batch that shares one cached prefix
+  gqa_key_weights / _paged the attention weight each cached key received
+  gqa_evict / _paged       the cache cut to a budget of keys by that weight
 """
 from __future__ import annotations
 
@@ -42,6 +50,7 @@ _DT = {torch.bfloat16: 0, torch.float32: 1}
 # Every symbol include/lka.h declares, with its ctypes signature (restype, argtypes).
 _P, _Z, _I, _F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 _FP = ctypes.POINTER(ctypes.c_float)
+_IP = ctypes.POINTER(ctypes.c_int64)
 SIGNATURES = {
     "gqa_attn_workspace_size": (_Z, [_I] * 6),
     "gqa_attn_split_count": (_I, [_I] * 7),
@@ -71,6 +80,21 @@ SIGNATURES = {
     "gta_shared_score_attn_paged_workspace_size": (_Z, [_I] * 8),
     "gta_shared_score_attn_paged": (_I, [_P] * 7 + [_I] * 10 + [_F, _I, _P, _Z, _P]),
     "latent_expand_cache": (_I, [_P] * 3 + [_I] * 6 + [_P] * 3 + [_I, _P]),
+    "rope_apply": (_I, [_P, _IP, _P, _P, _P, _IP] + [_I] * 7 + [_F, _I, _P]),
+    "gqa_rope_append": (_I, [_P] * 3 + [_IP] + [_P] * 6 + [_I] * 8 + [_F, _I, _P, _Z, _P]),
+    "gqa_rope_append_paged": (_I, [_P] * 3 + [_IP] + [_P] * 7 + [_I] * 10 + [_F, _I, _P, _Z, _P]),
+    "gqa_rope_append_fp8kv": (_I, [_P] * 3 + [_IP] + [_P] * 8 + [_I] * 8 + [_F, _P, _Z, _P]),
+    "latent_rope_append": (_I, [_P] * 3 + [_IP] + [_P] * 5 + [_I] * 7 + [_F, _I, _P, _Z, _P]),
+    "latent_rope_append_paged": (_I, [_P] * 3 + [_IP] + [_P] * 6 + [_I] * 9 + [_F, _I, _P, _Z, _P]),
+    "latent_rope_append_fp8kv": (_I, [_P] * 3 + [_IP] + [_P] * 6 + [_I] * 7 + [_F, _P, _Z, _P]),
+    "gqa_attn_shared_prefix_workspace_size": (_Z, [_I] * 8),
+    "gqa_attn_shared_prefix": (_I, [_P] * 9 + [_I] * 8 + [_F, _I, _P, _Z, _P]),
+    "gqa_attn_shared_prefix_paged_workspace_size": (_Z, [_I] * 9),
+    "gqa_attn_shared_prefix_paged": (_I, [_P] * 9 + [_I] * 10 + [_F, _I, _P, _Z, _P]),
+    "gqa_key_weights": (_I, [_P] * 5 + [_I] * 8 + [_F, _I, _P, _Z, _P]),
+    "gqa_key_weights_paged": (_I, [_P] * 6 + [_I] * 10 + [_F, _I, _P, _Z, _P]),
+    "gqa_evict": (_I, [_P] * 9 + [_I] * 9 + [_P, _Z, _P]),
+    "gqa_evict_paged": (_I, [_P] * 7 + [_I] * 10 + [_P, _Z, _P]),
     "lka_device_status": (_I, [_P, _P]),
     "lka_clear_status": (_I, [_P, _P]),
     "lka_status_string": (ctypes.c_char_p, [_I]),
@@ -519,16 +543,24 @@ def latent_expand_cache(latent, w_uk, w_uv):
 
 
 def device_status(device=None) -> int:
-    """Synchronises the current stream and returns the sticky status code of its workspace."""
+    """Synchronises the current stream and returns the sticky status code of its workspace, or else the one that the
+    captured calls of cache_ops share on the device."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     ws = workspaces.get(256, device)
-    return int(library().lka_device_status(_ptr(ws), _stream_ptr()))
+    code = int(library().lka_device_status(_ptr(ws), _stream_ptr()))
+    captured = cache_ops.captured_status(device)
+    if code == LKA_OK and captured is not None:
+        code = int(library().lka_device_status(_ptr(captured), _stream_ptr()))
+    return code
 
 
 def clear_status(device=None):
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     ws = workspaces.get(256, device)
     _check("lka_clear_status", library().lka_clear_status(_ptr(ws), _stream_ptr()))
+    captured = cache_ops.captured_status(device)
+    if captured is not None:
+        _check("lka_clear_status", library().lka_clear_status(_ptr(captured), _stream_ptr()))
 
 
 def gqa_split_count(B: int, h_q: int, h_kv: int, s_q: int, d: int, Lmax: int, dtype=torch.bfloat16) -> int:
@@ -556,3 +588,10 @@ def kernel_timing_read():
 
 def status_string(code: int) -> str:
     return library().lka_status_string(int(code)).decode()
+
+
+from . import cache_ops  # noqa: E402
+from .cache_ops import (gqa_attn_shared_prefix, gqa_attn_shared_prefix_paged, gqa_evict, gqa_evict_paged,  # noqa: E402,F401
+                        gqa_key_weights, gqa_key_weights_paged, gqa_rope_append, gqa_rope_append_fp8kv,
+                        gqa_rope_append_paged, latent_rope_append, latent_rope_append_fp8kv, latent_rope_append_paged,
+                        rope, rope_inv_freq)

@@ -1,0 +1,702 @@
+// prefix_attn.cu -- grouped-query attention of a batch that shares one cached prefix
+// (gqa_attn_shared_prefix, gqa_attn_shared_prefix_paged).
+//
+// Operation: every sequence attends over the keys of one prefix (length P, held once) and
+// over its own suffix (bottom-right causal, as gqa_attn).  Softmax over the union splits:
+//     out = sum_i 2^(m_i - m) l_i o_i / sum_i 2^(m_i - m) l_i
+// over parts i of the keys, with each part's maximum m_i, sum l_i and normalised o_i.  The
+// prefix parts are computed once for the whole batch: the query rows of all sequences that
+// use one KV head are the rows of one matrix product, so the prefix is read once per 16 to
+// 128 rows instead of once per sequence.
+//
+// Every part writes a normalised fp32 output and a log2-domain lse per row;
+// prefix_merge_kernel joins them and rounds once.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "mma.cuh"
+#include "prefix_attn.h"
+
+namespace lka {
+
+namespace {
+
+// ---- what a block works on ---------------------------------------------------------------------------------
+// Prefix: rows are the B * R query rows of a KV head (row i: sequence i / R, row i % R of its group).
+// Suffix: rows are the R rows of one sequence's group.  R = (h_q / h_kv) * s_q, row g is query g % s_q.
+struct Work {
+    bool prefix;
+    int kvh, b;        // b: the sequence of a suffix item
+    int row0, nrows;   // rows of the item (its row numbering), at most the block's rows
+    int kbeg, kend;    // keys
+    int slot;          // of the partial results
+    int L;             // length of the key sequence
+};
+
+// Item `idx` of the grid; false: nothing to do.
+__device__ __forceinline__ bool find_work(const PrefixParams& p, int rows_per_block, Work& w, bool report) {
+    int idx = blockIdx.x;
+    const int rb_pre = cdiv(p.B * p.R, rows_per_block), n_pre_items = p.do_prefix ? rb_pre * p.h_kv * p.n_pre : 0;
+    if (idx < n_pre_items) {
+        // row blocks of one (head, split) are neighbours: they read the same keys
+        const int rb = idx % rb_pre, split = (idx / rb_pre) % p.n_pre;
+        w.kvh = idx / (rb_pre * p.n_pre);
+        w.prefix = true;
+        w.b = 0;
+        w.row0 = rb * rows_per_block;
+        w.nrows = min(rows_per_block, p.B * p.R - w.row0);
+        w.L = prefix_length(p, report && idx == 0);
+        w.kbeg = split * p.pre_tokens;
+        w.kend = min(w.L, w.kbeg + p.pre_tokens);
+        w.slot = split;
+    } else {
+        idx -= n_pre_items;
+        const int rb_suf = cdiv(p.R, rows_per_block);
+        const int split = idx % p.n_suf, rb = (idx / p.n_suf) % rb_suf;
+        const int bh = idx / (p.n_suf * rb_suf);
+        w.kvh = bh % p.h_kv;
+        w.b = bh / p.h_kv;
+        w.prefix = false;
+        w.row0 = rb * rows_per_block;
+        w.nrows = min(rows_per_block, p.R - w.row0);
+        w.L = clamp_len(p.lens, w.b, p.Lmax, p.s, p.causal, p.status, report && w.kvh == 0 && rb == 0 && split == 0);
+        w.kbeg = split * p.suf_tokens;
+        w.kend = min(w.L, w.kbeg + p.suf_tokens);
+        w.slot = p.n_pre + split;
+    }
+    return w.kend > w.kbeg;
+}
+
+// Row `r` of the item in [B, h_q, s_q].
+__device__ __forceinline__ size_t global_row(const PrefixParams& p, const Work& w, int r) {
+    const int i = w.row0 + r;
+    const int b = w.prefix ? i / p.R : w.b, g = w.prefix ? i % p.R : i;
+    return ((size_t)b * p.h_kv + w.kvh) * p.R + g;
+}
+
+// Keys below this are visible to row `r`.
+__device__ __forceinline__ int visible_end(const PrefixParams& p, const Work& w, int r) {
+    if (w.prefix || !p.causal) return w.L;
+    return w.L - p.s + (w.row0 + r) % p.s + 1;
+}
+
+__device__ __forceinline__ CacheRows rows_of(const PrefixParams& p, const Work& w) {
+    CacheRows c;
+    c.page_size = p.page_size;
+    c.num_pages = p.num_pages;
+    c.heads = p.h_kv;
+    if (p.table) {
+        c.table = w.prefix ? p.ptable : p.table + (size_t)w.b * p.max_pages;
+        c.head_rows = w.kvh;
+    } else {
+        c.table = nullptr;
+        c.head_rows = w.prefix ? (long long)w.kvh * p.Lp : ((long long)w.b * p.h_kv + w.kvh) * p.Lmax;
+    }
+    return c;
+}
+
+// ---- bf16: warp-level MMAs ------------------------------------------------------------------------------------
+// ROWS4 = false: 16 query rows; the four warps take 16 keys each of a 64-key tile and join their states at the end.
+// ROWS4 = true: 64 query rows, 16 per warp, every warp takes the whole tile.
+template <int D, bool ROWS4>
+struct MmaCfg {
+    static constexpr int TK = 64, ROWS = ROWS4 ? 64 : 16;
+    static constexpr int KG = ROWS4 ? 4 : 1;            // 16-key groups of a tile per warp
+    static constexpr int STAGES = D == 64 ? 4 : 3;
+    static constexpr int MAT = TK * D * 2, STAGE = 2 * MAT, QB = ROWS * D * 2;
+    static constexpr int SMEM = QB + STAGES * STAGE;
+    // the merge of four warps' states reuses the stages: [4][16][D] fp32
+    static_assert(ROWS4 || 4 * 16 * D * 4 + 2 * 4 * 16 * 4 <= STAGES * STAGE, "merge scratch");
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+// Byte offset of 16-byte chunk c of row r: rows of D bf16 values, chunks permuted so that the 8 rows an ldmatrix
+// phase reads at one chunk lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+    return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) * 16));
+}
+
+template <int D, bool ROWS4>
+__global__ void __launch_bounds__(128) prefix_mma_kernel(const PrefixParams p) {
+    using C = MmaCfg<D, ROWS4>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+    Work w;
+    if (!find_work(p, C::ROWS, w, tid == 0)) return;
+    const CacheRows rows = rows_of(p, w);
+    const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(w.prefix ? p.kp : p.k);
+    const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(w.prefix ? p.vp : p.v);
+    const uint32_t sq = smem_u32(smem), st0 = sq + C::QB;
+
+    for (int i = tid; i < C::ROWS * (D / 8); i += 128) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        const bool ok = r < w.nrows;
+        cp_async16(sq + swz<D>(r, c), static_cast<const __nv_bfloat16*>(p.q) + (ok ? global_row(p, w, r) * D + c * 8 : 0), ok);
+    }
+    // keys and values of one tile; rows past the item's keys are zeros
+    auto load_tile = [&](int tile, int stage) {
+        const uint32_t dst = st0 + stage * C::STAGE;
+        const int k0 = w.kbeg + tile * C::TK;
+        constexpr int RPI = 128 / (D / 8);  // rows per pass of the block
+        const int c = tid % (D / 8);
+#pragma unroll
+        for (int r = tid / (D / 8); r < C::TK; r += RPI) {
+            const bool ok = k0 + r < w.kend;
+            const long long at = (ok ? cache_row(rows, k0 + r, p.status) : 0) * D + c * 8;
+            cp_async16(dst + swz<D>(r, c), kb + at, ok);
+            cp_async16(dst + C::MAT + swz<D>(r, c), vb + at, ok);
+        }
+    };
+    const int n_tiles = cdiv(w.kend - w.kbeg, C::TK);
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+        if (s < n_tiles) load_tile(s, s);
+        cp_async_commit();
+    }
+
+    const int row_w = ROWS4 ? warp * 16 : 0, key_w = ROWS4 ? 0 : warp * 16;
+    // this lane's rows are g and g + 8 of the warp's 16
+    int vis[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = row_w + g + 8 * h;
+        vis[h] = r < w.nrows ? min(visible_end(p, w, r), w.kend) : 0;
+    }
+    const int vis_all = __reduce_min_sync(0xffffffffu, min(vis[0], vis[1]));
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    constexpr bool QREG = D <= 128;  // the query fragments stay in registers
+    uint32_t qf[QREG ? D / 16 : 1][4];
+    const int arow = lane % 16, acol = lane / 16;  // ldmatrix addresses of a 16 x 16 A operand
+
+    for (int j = 0; j < n_tiles; ++j) {
+        cp_async_wait<C::STAGES - 2>();
+        __syncthreads();
+        if (j + C::STAGES - 1 < n_tiles) load_tile(j + C::STAGES - 1, (j + C::STAGES - 1) % C::STAGES);
+        cp_async_commit();
+        if constexpr (QREG) {
+            if (j == 0) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(qf[ks], sq + swz<D>(row_w + arow, 2 * ks + acol));
+            }
+        }
+        const uint32_t kt = st0 + (j % C::STAGES) * C::STAGE, vt = kt + C::MAT;
+        const int k0 = w.kbeg + j * C::TK + key_w;
+        // scores: KG groups of 16 keys, two 8-key column blocks each
+        float s[C::KG][2][4];
+#pragma unroll
+        for (int kg = 0; kg < C::KG; ++kg)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) s[kg][n][0] = s[kg][n][1] = s[kg][n][2] = s[kg][n][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t qa[4];
+            if constexpr (!QREG) ldmatrix4(qa, sq + swz<D>(row_w + arow, 2 * ks + acol));
+#pragma unroll
+            for (int kg = 0; kg < C::KG; ++kg) {
+                uint32_t kf[4];  // matrices: (keys 0-7, k 0-7), (keys 0-7, k 8-15), (keys 8-15, ..) x 2
+                ldmatrix4(kf, kt + swz<D>(key_w + kg * 16 + (lane / 16) * 8 + lane % 8, 2 * ks + (lane / 8) % 2));
+                mma_bf16(s[kg][0], QREG ? qf[QREG ? ks : 0] : qa, kf[0], kf[1]);
+                mma_bf16(s[kg][1], QREG ? qf[QREG ? ks : 0] : qa, kf[2], kf[3]);
+            }
+        }
+        // mask, running maximum
+        float mx[2] = {-INFINITY, -INFINITY};
+        const bool whole = k0 + 16 * C::KG <= vis_all;
+#pragma unroll
+        for (int kg = 0; kg < C::KG; ++kg)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[kg][n][e] * p.scale_log2;
+                    if (!whole && k0 + kg * 16 + n * 8 + 2 * t + (e & 1) >= vis[e / 2]) x = -INFINITY;
+                    s[kg][n][e] = x;
+                    mx[e / 2] = fmaxf(mx[e / 2], x);
+                }
+        bool grow = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            grow |= mx[h] > m[h];
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+            float al[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float mn = fmaxf(m[h], mx[h]);
+                al[h] = mn == -INFINITY ? 1.f : fast_exp2(m[h] - mn);
+                m[h] = mn;
+                l[h] *= al[h];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                o[i][0] *= al[0];
+                o[i][1] *= al[0];
+                o[i][2] *= al[1];
+                o[i][3] *= al[1];
+            }
+        }
+        const float ms[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        // P in the A layout of the value product (rounded to bf16 as everywhere in the library; the sums are of
+        // the fp32 values)
+#pragma unroll
+        for (int kg = 0; kg < C::KG; ++kg) {
+            uint32_t pa[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = fast_exp2(s[kg][n][i] - ms[i / 2]);
+                l[0] += e[0] + e[1];
+                l[1] += e[2] + e[3];
+                pa[2 * n] = bf16_pair(e[0], e[1]);
+                pa[2 * n + 1] = bf16_pair(e[2], e[3]);
+            }
+            const int vrow = key_w + kg * 16 + lane % 16;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t vf[4];  // transposed: (keys 0-7, 8-15) of value columns 16 i .. + 7, then .. + 15
+                ldmatrix4_t(vf, vt + swz<D>(vrow, 2 * i + lane / 16));
+                mma_bf16(o[2 * i], pa, vf[0], vf[1]);
+                mma_bf16(o[2 * i + 1], pa, vf[2], vf[3]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    if constexpr (ROWS4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = row_w + g + 8 * h;
+            if (r >= w.nrows) continue;
+            const size_t at = global_row(p, w, r) * p.n_slots + w.slot;
+            const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
+            float* po = p.part_o + at * D;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2*>(po + i * 8 + 2 * t) = make_float2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+            if (t == 0) p.part_lse[at] = l[h] > 0.f ? m[h] + log2f(l[h]) : -INFINITY;
+        }
+    } else {
+        __syncthreads();
+        float* om = reinterpret_cast<float*>(smem + C::QB);  // [4][16][D]
+        float* mm = om + 4 * 16 * D;                         // [4][16] maxima, then sums
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = warp * 16 + g + 8 * h;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2*>(om + r * D + i * 8 + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+            if (t == 0) {
+                mm[r] = m[h];
+                mm[64 + r] = l[h];
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < w.nrows * (D / 4); i += 128) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            float M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) M = fmaxf(M, mm[k * 16 + r]);
+            float sum = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = M == -INFINITY ? 0.f : fast_exp2(mm[k * 16 + r] - M);
+                const float4 x = *reinterpret_cast<const float4*>(om + (k * 16 + r) * D + c * 4);
+                sum += f * mm[64 + k * 16 + r];
+                a = make_float4(fmaf(f, x.x, a.x), fmaf(f, x.y, a.y), fmaf(f, x.z, a.z), fmaf(f, x.w, a.w));
+            }
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const size_t at = global_row(p, w, r) * p.n_slots + w.slot;
+            *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) =
+                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+            if (c == 0) p.part_lse[at] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+        }
+    }
+}
+
+// ---- fp32: CUDA cores ------------------------------------------------------------------------------------------
+// 16 query rows, four per warp; a tile of 32 keys, one key per lane for the scores, D / 32 value columns per lane.
+template <int D>
+struct F32Cfg {
+    static constexpr int TK = 32, ROWS = 16, KROW = D + 4;  // padded key rows: 16-byte reads of 8 lanes hit all banks
+    static constexpr int SMEM = (ROWS * D + TK * KROW + TK * D + ROWS * TK) * 4;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
+    using C = F32Cfg<D>;
+    constexpr int VPL = D / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* qs = reinterpret_cast<float*>(smem);
+    float* ks = qs + C::ROWS * D;
+    float* vs = ks + C::TK * C::KROW;
+    float* ps = vs + C::TK * D;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    Work w;
+    if (!find_work(p, C::ROWS, w, tid == 0)) return;
+    const CacheRows rows = rows_of(p, w);
+    const float* kb = static_cast<const float*>(w.prefix ? p.kp : p.k);
+    const float* vb = static_cast<const float*>(w.prefix ? p.vp : p.v);
+    for (int i = tid; i < C::ROWS * (D / 4); i += 128) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < w.nrows) x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + global_row(p, w, r) * D + c * 4);
+        *reinterpret_cast<float4*>(qs + r * D + c * 4) = x;
+    }
+    int vis[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int rr = warp * 4 + r;
+        vis[r] = rr < w.nrows ? min(visible_end(p, w, rr), w.kend) : 0;
+    }
+    float m[4], l[4], o[4][VPL];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) o[r][i] = 0.f;
+    }
+    for (int k0 = w.kbeg; k0 < w.kend; k0 += C::TK) {
+        __syncthreads();
+        for (int i = tid; i < C::TK * (D / 4); i += 128) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (k0 + r < w.kend) {
+                const long long at = cache_row(rows, k0 + r, p.status) * D + c * 4;
+                x = *reinterpret_cast<const float4*>(kb + at);
+                y = *reinterpret_cast<const float4*>(vb + at);
+            }
+            *reinterpret_cast<float4*>(ks + r * C::KROW + c * 4) = x;
+            *reinterpret_cast<float4*>(vs + r * D + c * 4) = y;
+        }
+        __syncthreads();
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const float* kp = ks + lane * C::KROW;
+        const float* qp = qs + warp * 4 * D;
+#pragma unroll 8
+        for (int c = 0; c < D; c += 4) {
+            const float4 kv = *reinterpret_cast<const float4*>(kp + c);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 qv = *reinterpret_cast<const float4*>(qp + r * D + c);
+                s[r] = fmaf(kv.x, qv.x, fmaf(kv.y, qv.y, fmaf(kv.z, qv.z, fmaf(kv.w, qv.w, s[r]))));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float x = k0 + lane < vis[r] ? s[r] * p.scale_log2 : -INFINITY;
+            float mx = x;
+#pragma unroll
+            for (int d = 16; d; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[r], mx);
+            const float al = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
+            const float e = mn == -INFINITY ? 0.f : exp2f(x - mn);
+            m[r] = mn;
+            l[r] = l[r] * al + e;
+            ps[(warp * 4 + r) * C::TK + lane] = e;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) o[r][i] *= al;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < C::TK; ++k) {
+            float v[VPL];
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) v[i] = vs[k * D + i * 32 + lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float e = ps[(warp * 4 + r) * C::TK + k];
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) o[r][i] = fmaf(e, v[i], o[r][i]);
+            }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int rr = warp * 4 + r;
+        float sum = l[r];
+#pragma unroll
+        for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (rr >= w.nrows) continue;
+        const size_t at = global_row(p, w, rr) * p.n_slots + w.slot;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) p.part_o[at * D + i * 32 + lane] = o[r][i] * inv;
+        if (lane == 0) p.part_lse[at] = sum > 0.f ? m[r] + log2f(sum) : -INFINITY;
+    }
+}
+
+// ---- the merge ---------------------------------------------------------------------------------------------------
+// D / 4 threads per row.  A row's parts are the prefix splits its length reaches and the suffix splits with a key
+// that the row sees.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p) {
+    constexpr int TPR = D / 4, RPB = 128 / TPR;
+    const size_t row = (size_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int c = threadIdx.x % TPR;
+    if (row >= (size_t)p.B * p.h_q * p.s) return;
+    const int b = (int)(row / ((size_t)p.h_q * p.s)), t = (int)(row % p.s);
+    const int P = prefix_length(p, false);
+    const int L = clamp_len(p.lens, b, p.Lmax, p.s, p.causal, p.status, false);
+    const int seen = p.causal ? L - p.s + t + 1 : L;
+    const int np = cdiv(P, p.pre_tokens), ns = cdiv(seen, p.suf_tokens);
+    const float* pl = p.part_lse + row * p.n_slots;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.n_slots * D) + c;
+    float M = -INFINITY;
+    for (int i = 0; i < np; ++i) M = fmaxf(M, pl[i]);
+    for (int i = 0; i < ns; ++i) M = fmaxf(M, pl[p.n_pre + i]);
+    float sum = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < np + ns; ++i) {
+        const int slot = i < np ? i : p.n_pre + i - np;
+        const float f = M == -INFINITY ? 0.f : exp2f(pl[slot] - M);
+        const float4 x = po[(size_t)slot * TPR];
+        sum += f;
+        a = make_float4(fmaf(f, x.x, a.x), fmaf(f, x.y, a.y), fmaf(f, x.z, a.z), fmaf(f, x.w, a.w));
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    T* out = static_cast<T*>(p.out) + row * D + c * 4;
+    if constexpr (sizeof(T) == 2) {
+        uint2 u;
+        u.x = bf16_pair(a.x * inv, a.y * inv);
+        u.y = bf16_pair(a.z * inv, a.w * inv);
+        *reinterpret_cast<uint2*>(out) = u;
+    } else {
+        *reinterpret_cast<float4*>(out) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    }
+    if (p.lse && c == 0) p.lse[row] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// ---- planning ------------------------------------------------------------------------------------------------------
+struct PrefixPlan {
+    int rows_pre, rows_suf;  // query rows per block of the prefix and the suffix kernel
+    int pre_tokens, n_pre, suf_tokens, n_suf;
+    size_t off_lse, off_o, ws_bytes;
+};
+
+// Keys per split of `units` row blocks over L keys: the split count n <= 64 that minimises waves x (tiles per split
+// + 2), the 2 for a block's start and end, where the waves of w = units n / slots cost max(ceil(w), w + 1/4).
+int split_keys(double units, double slots, int L, int tile) {
+    const int lt = cdiv(std::max(L, 1), tile);
+    int best = 1;
+    double best_cost = -1.0;
+    for (int n = 1; n <= lt && n <= 64; ++n) {
+        const double w = units * n / slots;
+        const double cost = fmax(ceil(w - 1e-9), w + 0.25) * (cdiv(lt, n) + 2);
+        if (best_cost < 0.0 || cost < best_cost - 1e-9) {
+            best_cost = cost;
+            best = n;
+        }
+    }
+    return cdiv(lt, best) * tile;
+}
+
+lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lmax, lka_dtype_t dtype, PrefixPlan* pl) {
+    if (B < 0 || h_q < 1 || h_kv < 1 || s < 1 || d < 1 || Lp < 0 || Lmax < 1 || h_q % h_kv) return LKA_ERR_INVALID_ARG;
+    if (dtype != LKA_BF16 && dtype != LKA_FP32) return LKA_ERR_UNSUPPORTED;
+    if (!(d == 64 || d == 128 || (d == 256 && dtype == LKA_BF16))) return LKA_ERR_UNSUPPORTED;
+    if ((long long)B * h_q * s >= (1ll << 28) || Lp > (1 << 30) || Lmax > (1 << 30)) return LKA_ERR_UNSUPPORTED;
+    const int R = h_q / h_kv * s, Bn = std::max(B, 1);
+    const bool f32 = dtype == LKA_FP32;
+    // up to 16 rows in all, the four warps split the keys; more, they split the rows and the prefix is read once
+    // per 64 of them
+    pl->rows_pre = f32 || Bn * R <= 16 ? 16 : 64;
+    pl->rows_suf = 16;
+    const int tile = f32 ? 32 : 64;
+    const double slots = (double)sm_count() * (f32 ? 3 : d == 256 ? 1 : 2);
+    const int knob = split_tokens_knob();
+    pl->pre_tokens = knob > 0 ? cdiv(knob, tile) * tile
+                              : split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile);
+    pl->suf_tokens = knob > 0 ? cdiv(knob, tile) * tile
+                              : split_keys((double)h_kv * Bn * cdiv(R, pl->rows_suf), slots, Lmax, tile);
+    pl->n_pre = cdiv(Lp, pl->pre_tokens);
+    pl->n_suf = cdiv(Lmax, pl->suf_tokens);
+    WsCarve c;
+    const size_t rows = (size_t)B * h_q * s, slots_n = (size_t)pl->n_pre + pl->n_suf;
+    pl->off_lse = c.take(rows * slots_n * sizeof(float));
+    pl->off_o = c.take(rows * slots_n * d * sizeof(float));
+    pl->ws_bytes = c.off;
+    return LKA_OK;
+}
+
+template <typename K>
+cudaError_t launch_attn(K kern, int smem, const PrefixParams& p, int rows, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long n = (p.do_prefix ? (long long)cdiv(p.B * p.R, rows) * p.h_kv * p.n_pre : 0) +
+                        (p.do_suffix ? (long long)p.B * p.h_kv * cdiv(p.R, rows) * p.n_suf : 0);
+    if (n == 0) return cudaSuccess;
+    if (n >= (1ll << 31)) return cudaErrorInvalidValue;
+    kern<<<(unsigned)n, 128, smem, st>>>(p);
+    return cudaPeekAtLastError();
+}
+
+template <int D>
+cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
+    TimedLaunch timer(st);
+    cudaError_t e = cudaSuccess;
+    if (pl.rows_pre > 16) {
+        p.do_suffix = 0;
+        e = launch_attn(prefix_mma_kernel<D, true>, MmaCfg<D, true>::SMEM, p, 64, st);
+        p.do_suffix = 1;
+        p.do_prefix = 0;
+    }
+    if (e == cudaSuccess) e = launch_attn(prefix_mma_kernel<D, false>, MmaCfg<D, false>::SMEM, p, 16, st);
+    timer.stop();
+    if (e != cudaSuccess) return e;
+    const size_t rows = (size_t)p.B * p.h_q * p.s;
+    constexpr int RPB = 128 / (D / 4);
+    prefix_merge_kernel<__nv_bfloat16, D><<<(unsigned)((rows + RPB - 1) / RPB), 128, 0, st>>>(p);
+    return cudaPeekAtLastError();
+}
+
+template <int D>
+cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
+    TimedLaunch timer(st);
+    const cudaError_t e = launch_attn(prefix_f32_kernel<D>, F32Cfg<D>::SMEM, p, 16, st);
+    timer.stop();
+    if (e != cudaSuccess) return e;
+    const size_t rows = (size_t)p.B * p.h_q * p.s;
+    constexpr int RPB = 128 / (D / 4);
+    prefix_merge_kernel<float, D><<<(unsigned)((rows + RPB - 1) / RPB), 128, 0, st>>>(p);
+    return cudaPeekAtLastError();
+}
+
+lka_status_t prefix_run(PrefixParams& p, int d, float scale, lka_dtype_t dtype, void* ws, size_t ws_bytes,
+                        void* stream) {
+    PrefixPlan pl;
+    lka_status_t r = prefix_plan(p.B, p.h_q, p.h_kv, p.s, d, p.Lp, p.Lmax, dtype, &pl);
+    if (r != LKA_OK) return r;
+    if (p.B == 0) return LKA_OK;
+    const void* ptrs[] = {p.q, p.k, p.v, p.out, p.lens};
+    for (const void* x : ptrs)
+        if (!x || !aligned16(x)) return LKA_ERR_INVALID_ARG;
+    if (p.Lp > 0 && (!p.kp || !p.vp || !aligned16(p.kp) || !aligned16(p.vp))) return LKA_ERR_INVALID_ARG;
+    if (p.prefix_len && (reinterpret_cast<uintptr_t>(p.prefix_len) & 3u)) return LKA_ERR_INVALID_ARG;
+    if (p.lse && (reinterpret_cast<uintptr_t>(p.lse) & 3u)) return LKA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return LKA_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < pl.ws_bytes) return LKA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return LKA_ERR_INVALID_ARG;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    p.status = reinterpret_cast<uint32_t*>(w);
+    p.part_lse = reinterpret_cast<float*>(w + pl.off_lse);
+    p.part_o = reinterpret_cast<float*>(w + pl.off_o);
+    p.ratio = p.h_q / p.h_kv;
+    p.R = p.ratio * p.s;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.pre_tokens = pl.pre_tokens;
+    p.n_pre = pl.n_pre;
+    p.suf_tokens = pl.suf_tokens;
+    p.n_suf = pl.n_suf;
+    p.n_slots = pl.n_pre + pl.n_suf;
+    p.do_prefix = p.do_suffix = 1;
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (dtype == LKA_FP32)
+        e = d == 64 ? run_f32<64>(p, st) : run_f32<128>(p, st);
+    else
+        e = d == 64 ? run_bf16<64>(p, pl, st) : d == 128 ? run_bf16<128>(p, pl, st) : run_bf16<256>(p, pl, st);
+    return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+}
+
+bool prefix_pages_ok(int page_size, int max_prefix_pages, int max_pages, int num_pages) {
+    return page_size >= 8 && (page_size & (page_size - 1)) == 0 && max_prefix_pages >= 0 && max_pages >= 1 &&
+           num_pages >= 1 && (long long)max_pages * page_size <= (1 << 30) &&
+           (long long)max_prefix_pages * page_size <= (1 << 30);
+}
+
+}  // namespace
+}  // namespace lka
+
+using namespace lka;
+
+extern "C" {
+
+size_t gqa_attn_shared_prefix_workspace_size(int B, int h_q, int h_kv, int s_q, int d_h, int Lp, int Lmax,
+                                             lka_dtype_t dtype) {
+    PrefixPlan pl;
+    return prefix_plan(B, h_q, h_kv, s_q, d_h, Lp, Lmax, dtype, &pl) == LKA_OK ? pl.ws_bytes : 0;
+}
+
+lka_status_t gqa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix,
+                                    const int32_t* prefix_len, const void* k, const void* v, const int32_t* cache_lens,
+                                    void* out, float* lse, int B, int h_q, int h_kv, int s_q, int d_h, int Lp,
+                                    int Lmax, int causal, float scale, lka_dtype_t dtype, void* ws, size_t ws_bytes,
+                                    void* stream) {
+    PrefixParams p{};
+    p.q = q;
+    p.kp = k_prefix;
+    p.vp = v_prefix;
+    p.prefix_len = prefix_len;
+    p.k = k;
+    p.v = v;
+    p.lens = cache_lens;
+    p.out = out;
+    p.lse = lse;
+    p.B = B;
+    p.h_q = h_q;
+    p.h_kv = h_kv;
+    p.s = s_q;
+    p.Lp = Lp;
+    p.Lmax = Lmax;
+    p.causal = causal ? 1 : 0;
+    return prefix_run(p, d_h, scale, dtype, ws, ws_bytes, stream);
+}
+
+size_t gqa_attn_shared_prefix_paged_workspace_size(int B, int h_q, int h_kv, int s_q, int d_h, int page_size,
+                                                   int max_prefix_pages, int max_pages, lka_dtype_t dtype) {
+    if (!prefix_pages_ok(page_size, max_prefix_pages, max_pages, 1)) return 0;
+    return gqa_attn_shared_prefix_workspace_size(B, h_q, h_kv, s_q, d_h, page_size * max_prefix_pages,
+                                                 page_size * max_pages, dtype);
+}
+
+lka_status_t gqa_attn_shared_prefix_paged(const void* q, const void* k_pages, const void* v_pages,
+                                          const int32_t* prefix_table, const int32_t* prefix_len,
+                                          const int32_t* block_table, const int32_t* cache_lens, void* out, float* lse,
+                                          int B, int h_q, int h_kv, int s_q, int d_h, int page_size,
+                                          int max_prefix_pages, int max_pages, int num_pages, int causal, float scale,
+                                          lka_dtype_t dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (!prefix_pages_ok(page_size, max_prefix_pages, max_pages, num_pages)) return LKA_ERR_INVALID_ARG;
+    if (B > 0 && (!block_table || (reinterpret_cast<uintptr_t>(block_table) & 3u))) return LKA_ERR_INVALID_ARG;
+    if (B > 0 && max_prefix_pages > 0 && (!prefix_table || (reinterpret_cast<uintptr_t>(prefix_table) & 3u)))
+        return LKA_ERR_INVALID_ARG;
+    PrefixParams p{};
+    p.q = q;
+    p.kp = p.k = k_pages;
+    p.vp = p.v = v_pages;
+    p.ptable = prefix_table;
+    p.prefix_len = prefix_len;
+    p.table = block_table;
+    p.lens = cache_lens;
+    p.out = out;
+    p.lse = lse;
+    p.B = B;
+    p.h_q = h_q;
+    p.h_kv = h_kv;
+    p.s = s_q;
+    p.Lp = page_size * max_prefix_pages;
+    p.Lmax = page_size * max_pages;
+    p.causal = causal ? 1 : 0;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    return prefix_run(p, d_h, scale, dtype, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

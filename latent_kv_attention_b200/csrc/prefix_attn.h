@@ -1,0 +1,36 @@
+// prefix_attn.h -- parameters of the shared-prefix attention kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace lka {
+
+struct PrefixParams {
+    const void* q;               // [B, h_q, s, D]
+    const void *kp, *vp;         // prefix: [h_kv, Lp, D], or the page pools
+    const void *k, *v;           // suffixes: [B, h_kv, Lmax, D], or the page pools
+    const int32_t* prefix_len;   // device [1], or null: Lp
+    const int32_t* lens;         // device [B], suffix lengths
+    const int32_t *ptable, *table;  // paged: [max_prefix_pages] and [B, max_pages]; null: contiguous
+    void* out;                   // [B, h_q, s, D]
+    float* lse;                  // [B, h_q, s] natural log, or null
+    float *part_o, *part_lse;    // [B * h_q * s][n_slots][D] and [..][n_slots] (log2 domain)
+    uint32_t* status;
+    int B, h_q, h_kv, s, ratio, R, Lp, Lmax, causal;
+    int pre_tokens, n_pre, suf_tokens, n_suf, n_slots;
+    int do_prefix, do_suffix;    // which items a launch holds
+    int page_size, max_pages, num_pages;
+    float scale_log2;
+};
+
+// The prefix length, clamped into [0, Lp].
+__device__ __forceinline__ int prefix_length(const PrefixParams& p, bool report) {
+    int P = p.prefix_len ? *p.prefix_len : p.Lp;
+    if (P < 0 || P > p.Lp) {
+        if (report) atomicOr(p.status, kDevBadLength);
+        P = P < 0 ? 0 : p.Lp;
+    }
+    return P;
+}
+
+}  // namespace lka

@@ -1,0 +1,542 @@
+// rope.cu -- rotary positions, alone (rope_apply) and fused with the write of
+// a step's new keys and values into the cache (gqa_rope_append*, latent_rope_append*).
+//
+// Operation: pair i (0 <= i < n) of a head at position p is turned by the angle
+// p * inv_freq[i] and scaled by `amplitude` a:
+//     y0 = a (x0 cos - x1 sin),  y1 = a (x1 cos + x0 sin)
+// with (x0, x1) = (x[i], x[i + n]) (half layout) or (x[2i], x[2i + 1])
+// (interleaved); values from 2n on pass through.  The rotation is orthogonal, so
+// its backward pass is the same with sin negated (the transpose of a R(p) is a R(-p)).
+//
+// Angles of far positions lose their fraction of a turn in fp32 (p = 10^6 leaves
+// 2^-4 rad), so the turn count p * inv_freq / 2 pi is formed in fp64, reduced to
+// [-1/2, 1/2] there, and only the reduced turn goes to fp32 (sincospi): two fp64
+// operations per (token, pair), shared by every head of the token.
+//
+// Bound: HBM (about 0.75 operations per byte moved), or launch latency for a
+// decode step.  One CTA takes one token (its cos / sin table is made once, in
+// shared memory, for all heads); each thread moves units of two 16-byte vectors
+// (the two halves of VE pairs, or 2 VE pairs side by side), issues the loads of up
+// to four units before it computes, and rounds once, on the way out.  While there
+// are few tokens, the units of one token are spread over several CTAs instead.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "host_util.h"
+
+namespace lka {
+
+struct RopeStrides {
+    int64_t b, h, s;  // in elements; the head dim is contiguous
+};
+
+struct RopeParams {
+    const void *q, *k, *v;  // [B, heads, s, d] through strides; k, v null for rope_apply
+    void* q_out;
+    RopeStrides qs, ks, vs, os;
+    void *kc, *vc;                          // cache bases (k already offset to its column)
+    int64_t slab, k_head, v_head, row;      // cache strides in elements: sequence or page, head, token row
+    const float *k_scale, *v_scale;         // e4m3 caches: per head (scale_by_head) or one value
+    int scale_by_head;
+    const int32_t* lens;       // null for rope_apply
+    const int32_t* positions;  // [B, s] or null: the token's cache row
+    const double* inv_freq;    // [n] radians per token
+    const int32_t* table;      // paged: [B, max_pages]
+    uint32_t* status;
+    int B, s, h_q, h_kv, d, dv, n, Lmax, page_size, max_pages, num_pages;
+    float amplitude;
+    float sign;  // +1, or -1 for the backward pass
+    int units, units_per_cta;
+};
+
+namespace {
+
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 4;     // units in flight per thread
+constexpr int kRopeMaxPairs = 256;
+
+template <typename T, int VE>
+struct VecOf;
+template <>
+struct VecOf<__nv_bfloat16, 8> { using V = uint4; };
+template <>
+struct VecOf<float, 4> { using V = uint4; };
+template <>
+struct VecOf<__nv_bfloat16, 1> { using V = uint16_t; };
+template <>
+struct VecOf<float, 1> { using V = uint32_t; };
+
+template <typename T, int VE>
+__device__ __forceinline__ void unpack(const typename VecOf<T, VE>::V& u, float* f) {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) f[i] = to_f32<T>(e[i]);
+}
+
+// VE values to the destination type, in one store.  e4m3: value / scale, rounded to nearest even, saturated.
+template <typename C, int VE>
+__device__ __forceinline__ void store_vec(void* base, long long at, const float* f, float scale) {
+    if constexpr (sizeof(C) == 1) {
+        uint8_t b[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            b[i] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(f[i], scale), __NV_SATFINITE, __NV_E4M3);
+        uint8_t* p = static_cast<uint8_t*>(base) + at;
+        if constexpr (VE == 8)
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(b);
+        else
+            p[0] = b[0];
+    } else {
+        typename VecOf<C, VE>::V u;
+        C* e = reinterpret_cast<C*>(&u);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) e[i] = from_f32<C>(f[i]);
+        *reinterpret_cast<typename VecOf<C, VE>::V*>(static_cast<C*>(base) + at) = u;
+    }
+}
+
+// Units of one head of d values: the n pairs in groups of VE, then the values past 2n in groups of 2 VE.
+__host__ __device__ inline int rot_units(int n, int ve) { return (n + ve - 1) / ve; }
+__host__ __device__ inline int copy_units(int values, int ve) { return (values + 2 * ve - 1) / (2 * ve); }
+
+// T: element of q, k, v and q_out; C: element of the cache; VE: values per vector (1: no alignment needed).
+template <typename T, typename C, int VE, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+    using V = typename VecOf<T, VE>::V;
+    __shared__ float2 cs[kRopeMaxPairs];
+    const int tok = blockIdx.x, b = tok / p.s, t = tok % p.s;
+
+    // the token's cache row (-1: a padding token, or one whose place is not in the cache)
+    int row = t, slab = b;
+    bool live = true;
+    if (p.lens) {
+        const int L = p.lens[b];
+        const bool bad = L < 0 || L > p.Lmax;
+        if (bad && t == 0 && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, kDevBadLength);
+        row = L - p.s + t;
+        live = !bad && row >= 0;
+    }
+    bool store = live;
+    int in_slab = row;
+    if (p.table && live) {
+        const int page = p.table[(size_t)b * p.max_pages + row / p.page_size];
+        if (page < 0 || page >= p.num_pages) {
+            if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, kDevBadPage);
+            store = false;
+        }
+        slab = page;
+        in_slab = row % p.page_size;
+    }
+
+    const int nrot = rot_units(p.n, VE), upq = nrot + copy_units(p.d - 2 * p.n, VE);
+    const int upv = p.v ? copy_units(p.dv, VE) : 0;
+    const int uq = p.h_q * upq, uk = p.k ? p.h_kv * upq : 0;
+    const int u_end = min(p.units, ((int)blockIdx.y + 1) * p.units_per_cta);
+    bool have_table = false;
+
+    for (int u0 = blockIdx.y * p.units_per_cta; u0 < u_end; u0 += kRopeThreads * kRopeBatch) {
+        V x[kRopeBatch][2];
+#pragma unroll
+        for (int j = 0; j < kRopeBatch; ++j) {
+            const int u = u0 + j * kRopeThreads + threadIdx.x;
+            x[j][0] = V{};
+            x[j][1] = V{};
+            if (u >= u_end || !live) continue;
+            const T* src;
+            int w, c0, c1, width = p.d;  // unit in the head, columns of its two vectors
+            if (u < uq) {
+                const int h = u / upq;
+                w = u - h * upq;
+                src = static_cast<const T*>(p.q) + b * p.qs.b + h * p.qs.h + t * p.qs.s;
+            } else if (u < uq + uk) {
+                const int h = (u - uq) / upq;
+                w = u - uq - h * upq;
+                src = static_cast<const T*>(p.k) + b * p.ks.b + h * p.ks.h + t * p.ks.s;
+            } else {
+                const int h = (u - uq - uk) / upv;
+                w = u - uq - uk - h * upv + nrot;
+                src = static_cast<const T*>(p.v) + b * p.vs.b + h * p.vs.h + t * p.vs.s;
+                width = p.dv;
+            }
+            if (w < nrot) {
+                c0 = INTER ? 2 * VE * w : VE * w;
+                c1 = INTER ? c0 + VE : c0 + p.n;
+            } else {
+                c0 = (u < uq + uk ? 2 * p.n : 0) + 2 * VE * (w - nrot);
+                c1 = c0 + VE;
+            }
+            x[j][0] = *reinterpret_cast<const V*>(src + c0);
+            if (c1 < width) x[j][1] = *reinterpret_cast<const V*>(src + c1);
+        }
+        if (!have_table) {
+            if (live) {
+                const double pos = p.positions ? (double)p.positions[(size_t)b * p.s + t] : (double)row;
+                for (int i = threadIdx.x; i < p.n; i += kRopeThreads) {
+                    const double turn = pos * (p.inv_freq[i] * 0.15915494309189533577);
+                    float sn, cn;
+                    sincospif(2.0f * (float)(turn - rint(turn)), &sn, &cn);
+                    cs[i] = make_float2(cn * p.amplitude, sn * p.amplitude * p.sign);
+                }
+            }
+            __syncthreads();
+            have_table = true;
+        }
+#pragma unroll
+        for (int j = 0; j < kRopeBatch; ++j) {
+            const int u = u0 + j * kRopeThreads + threadIdx.x;
+            if (u >= u_end) continue;
+            float a[VE], c[VE];
+            unpack<T, VE>(x[j][0], a);
+            unpack<T, VE>(x[j][1], c);
+            const bool is_q = u < uq, is_v = u >= uq + uk;
+            const int per = is_v ? upv : upq, first = is_q ? 0 : is_v ? uq + uk : uq;
+            const int h = (u - first) / per, w = u - first - h * per;
+            const bool turn = !is_v && w < nrot;
+            int c0, c1;
+            if (turn) {
+                c0 = INTER ? 2 * VE * w : VE * w;
+                c1 = INTER ? c0 + VE : c0 + p.n;
+                if constexpr (INTER) {
+                    // pairs lie side by side in the 2 VE values
+                    float z[2 * VE];
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        z[i] = a[i];
+                        z[VE + i] = c[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        const float2 r = live ? cs[VE * w + i] : make_float2(0.f, 0.f);
+                        const float x0 = z[2 * i], x1 = z[2 * i + 1];
+                        z[2 * i] = x0 * r.x - x1 * r.y;
+                        z[2 * i + 1] = x1 * r.x + x0 * r.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        a[i] = z[i];
+                        c[i] = z[VE + i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        const float2 r = live ? cs[VE * w + i] : make_float2(0.f, 0.f);
+                        const float x0 = a[i], x1 = c[i];
+                        a[i] = x0 * r.x - x1 * r.y;
+                        c[i] = x1 * r.x + x0 * r.y;
+                    }
+                }
+            } else {
+                c0 = is_v ? 2 * VE * w : 2 * p.n + 2 * VE * (w - nrot);
+                c1 = c0 + VE;
+            }
+            const int width = is_v ? p.dv : p.d;
+            if (is_q) {
+                const long long o = b * p.os.b + h * p.os.h + t * p.os.s;
+                store_vec<T, VE>(p.q_out, o + c0, a, 1.f);
+                if (c1 < width) store_vec<T, VE>(p.q_out, o + c1, c, 1.f);
+            } else if (store) {
+                const float* sc = is_v ? p.v_scale : p.k_scale;
+                const float scale = sizeof(C) == 1 ? sc[p.scale_by_head ? h : 0] : 1.f;
+                void* base = is_v ? p.vc : p.kc;
+                const long long o = slab * p.slab + h * (is_v ? p.v_head : p.k_head) + in_slab * p.row;
+                store_vec<C, VE>(base, o + c0, a, scale);
+                if (c1 < width) store_vec<C, VE>(base, o + c1, c, scale);
+            }
+        }
+    }
+}
+
+bool vec_ok(const void* ptr, int bytes) { return (reinterpret_cast<uintptr_t>(ptr) % bytes) == 0; }
+bool strides_ok(const RopeStrides& s, int ve) { return s.b % ve == 0 && s.h % ve == 0 && s.s % ve == 0; }
+
+template <typename T, typename C>
+cudaError_t rope_launch(RopeParams& p, bool inter, cudaStream_t st) {
+    constexpr int W = 16 / (int)sizeof(T);
+    // the vector path wants every vector 16-byte aligned on the way in and whole on the way out; head dims and
+    // strides that are not multiples of it take one value at a time
+    const int cw = W * (int)sizeof(C);
+    bool vec = p.n % W == 0 && p.d % W == 0 && vec_ok(p.q, 16) && vec_ok(p.q_out, 16) && strides_ok(p.qs, W) &&
+               strides_ok(p.os, W);
+    if (p.k) {
+        vec = vec && vec_ok(p.k, 16) && strides_ok(p.ks, W) && vec_ok(p.kc, cw) && p.slab % W == 0 &&
+              p.k_head % W == 0 && p.row % W == 0;
+        vec = vec && p.dv % W == 0 && vec_ok(p.v, 16) && strides_ok(p.vs, W) && vec_ok(p.vc, cw) && p.v_head % W == 0;
+    }
+    const int ve = vec ? W : 1;
+    const int upq = rot_units(p.n, ve) + copy_units(p.d - 2 * p.n, ve);
+    const long long units = (long long)(p.h_q + (p.k ? p.h_kv : 0)) * upq +
+                            (p.v ? (long long)p.h_kv * copy_units(p.dv, ve) : 0);
+    if (units >= (1ll << 31)) return cudaErrorInvalidValue;
+    p.units = (int)units;
+    const long long tokens = (long long)p.B * p.s;
+    // few tokens: one batch of loads per thread at most, spread over the SMs; many: one CTA per token
+    p.units_per_cta = p.units;
+    if (tokens < 4LL * sm_count()) {
+        const int want = (int)((4LL * sm_count() + tokens - 1) / tokens);
+        p.units_per_cta = std::max(kRopeThreads, cdiv(p.units, want));
+    }
+    p.units_per_cta = std::max(p.units_per_cta, cdiv(p.units, 32768));
+    const dim3 grid((unsigned)tokens, cdiv(p.units, p.units_per_cta));
+    TimedLaunch timer(st);
+    if (vec) {
+        if (inter)
+            rope_kernel<T, C, W, true><<<grid, kRopeThreads, 0, st>>>(p);
+        else
+            rope_kernel<T, C, W, false><<<grid, kRopeThreads, 0, st>>>(p);
+    } else {
+        if (inter)
+            rope_kernel<T, C, 1, true><<<grid, kRopeThreads, 0, st>>>(p);
+        else
+            rope_kernel<T, C, 1, false><<<grid, kRopeThreads, 0, st>>>(p);
+    }
+    timer.stop();
+    return cudaPeekAtLastError();
+}
+
+lka_status_t launch_status(cudaError_t e) { return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA; }
+
+bool elem_aligned(const void* ptr, int bytes) { return ptr && (reinterpret_cast<uintptr_t>(ptr) % bytes) == 0; }
+
+// What every form checks of the sizes: rotated width d_rot of heads of d values.
+lka_status_t rope_sizes(int B, int h, int s, int d, int d_rot, float amplitude) {
+    if (B < 0 || h < 1 || s < 1 || d < 1 || d_rot < 2 || d_rot % 2 || d_rot > d) return LKA_ERR_INVALID_ARG;
+    if (!(amplitude == amplitude) || amplitude - amplitude != 0.f) return LKA_ERR_INVALID_ARG;
+    if (d_rot / 2 > kRopeMaxPairs || d > 65536 || h > 65536) return LKA_ERR_UNSUPPORTED;
+    if ((long long)B * s >= (1ll << 31)) return LKA_ERR_UNSUPPORTED;
+    return LKA_OK;
+}
+
+struct CacheDesc {
+    void *kc, *vc;
+    int64_t slab, k_head, v_head, row;
+    const float *k_scale, *v_scale;
+    bool fp8;
+    int scale_by_head;
+    int dv;
+    const int32_t* table;
+    int page_size, max_pages, num_pages;
+};
+
+lka_status_t append_run(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* lens,
+                        const int32_t* positions, const double* inv_freq, void* q_out, int B, int h_q, int h_kv, int s,
+                        int d, int d_rot, int Lmax, int interleaved, float amplitude, lka_dtype_t dtype,
+                        const CacheDesc& c, void* ws, size_t ws_bytes, void* stream) {
+    lka_status_t r = rope_sizes(B, h_q, s, d, d_rot, amplitude);
+    if (r != LKA_OK) return r;
+    if (h_kv < 1 || Lmax < 1 || c.dv < 1) return LKA_ERR_INVALID_ARG;
+    if (dtype != LKA_BF16 && dtype != LKA_FP32) return LKA_ERR_UNSUPPORTED;
+    if (c.fp8 && dtype != LKA_BF16) return LKA_ERR_UNSUPPORTED;
+    if (h_kv > 65536 || c.dv > 65536) return LKA_ERR_UNSUPPORTED;
+    if (B == 0) return LKA_OK;
+    const int eb = dtype == LKA_BF16 ? 2 : 4, cb = c.fp8 ? 1 : eb;
+    if (!strides || !elem_aligned(q, eb) || !elem_aligned(k, eb) || !elem_aligned(v, eb) || !elem_aligned(q_out, eb) ||
+        !elem_aligned(c.kc, cb) || !elem_aligned(c.vc, cb) || !elem_aligned(lens, 4) || !elem_aligned(inv_freq, 8))
+        return LKA_ERR_INVALID_ARG;
+    if (positions && !elem_aligned(positions, 4)) return LKA_ERR_INVALID_ARG;
+    if (c.fp8 && (!elem_aligned(c.k_scale, 4) || !elem_aligned(c.v_scale, 4))) return LKA_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < kWsHeaderBytes) return LKA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return LKA_ERR_INVALID_ARG;
+    RopeParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.qs = {strides[0], strides[1], strides[2]};
+    p.ks = {strides[3], strides[4], strides[5]};
+    p.vs = {strides[6], strides[7], strides[8]};
+    p.os = {(int64_t)h_q * s * d, (int64_t)s * d, d};
+    p.kc = c.kc;
+    p.vc = c.vc;
+    p.slab = c.slab;
+    p.k_head = c.k_head;
+    p.v_head = c.v_head;
+    p.row = c.row;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.scale_by_head = c.scale_by_head;
+    p.lens = lens;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.table = c.table;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages;
+    p.num_pages = c.num_pages;
+    p.status = static_cast<uint32_t*>(ws);
+    p.B = B;
+    p.s = s;
+    p.h_q = h_q;
+    p.h_kv = h_kv;
+    p.d = d;
+    p.dv = c.dv;
+    p.n = d_rot / 2;
+    p.Lmax = Lmax;
+    p.amplitude = amplitude;
+    p.sign = 1.f;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const bool inter = interleaved != 0;
+    if (c.fp8) return launch_status(rope_launch<__nv_bfloat16, __nv_fp8_e4m3>(p, inter, st));
+    if (dtype == LKA_BF16) return launch_status(rope_launch<__nv_bfloat16, __nv_bfloat16>(p, inter, st));
+    return launch_status(rope_launch<float, float>(p, inter, st));
+}
+
+bool rope_pages_ok(const int32_t* table, int B, int page_size, int max_pages, int num_pages) {
+    return page_size >= 8 && (page_size & (page_size - 1)) == 0 && max_pages >= 1 && num_pages >= 1 &&
+           (long long)max_pages * page_size < (1ll << 31) && (B <= 0 || elem_aligned(table, 4));
+}
+
+}  // namespace
+}  // namespace lka
+
+using namespace lka;
+
+extern "C" {
+
+lka_status_t rope_apply(const void* x, const int64_t* x_strides, const int32_t* positions, const double* inv_freq,
+                        void* out, const int64_t* out_strides, int B, int h, int s, int d, int d_rot, int interleaved,
+                        int backward, float amplitude, lka_dtype_t dtype, void* stream) {
+    lka_status_t r = rope_sizes(B, h, s, d, d_rot, amplitude);
+    if (r != LKA_OK) return r;
+    if (dtype != LKA_BF16 && dtype != LKA_FP32) return LKA_ERR_UNSUPPORTED;
+    if (B == 0) return LKA_OK;
+    const int eb = dtype == LKA_BF16 ? 2 : 4;
+    if (!x_strides || !out_strides || !elem_aligned(x, eb) || !elem_aligned(out, eb) || !elem_aligned(positions, 4) ||
+        !elem_aligned(inv_freq, 8))
+        return LKA_ERR_INVALID_ARG;
+    RopeParams p{};
+    p.q = x;
+    p.q_out = out;
+    p.qs = {x_strides[0], x_strides[1], x_strides[2]};
+    p.os = {out_strides[0], out_strides[1], out_strides[2]};
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.B = B;
+    p.s = s;
+    p.h_q = h;
+    p.d = d;
+    p.n = d_rot / 2;
+    p.amplitude = amplitude;
+    p.sign = backward ? -1.f : 1.f;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (dtype == LKA_BF16) return launch_status(rope_launch<__nv_bfloat16, __nv_bfloat16>(p, interleaved != 0, st));
+    return launch_status(rope_launch<float, float>(p, interleaved != 0, st));
+}
+
+lka_status_t gqa_rope_append(const void* q, const void* k, const void* v, const int64_t* strides,
+                             const int32_t* cache_lens, const int32_t* positions, const double* inv_freq, void* q_out,
+                             void* k_cache, void* v_cache, int B, int h_q, int h_kv, int s_q, int d_h, int d_rot,
+                             int Lmax, int interleaved, float amplitude, lka_dtype_t dtype, void* ws, size_t ws_bytes,
+                             void* stream) {
+    CacheDesc c{};
+    c.kc = k_cache;
+    c.vc = v_cache;
+    c.slab = (long long)h_kv * Lmax * d_h;
+    c.k_head = c.v_head = (long long)Lmax * d_h;
+    c.row = c.dv = d_h;
+    return append_run(q, k, v, strides, cache_lens, positions, inv_freq, q_out, B,
+                      h_q, h_kv, s_q, d_h, d_rot, Lmax, interleaved, amplitude, dtype, c, ws, ws_bytes, stream);
+}
+
+lka_status_t gqa_rope_append_paged(const void* q, const void* k, const void* v, const int64_t* strides,
+                                   const int32_t* block_table, const int32_t* cache_lens, const int32_t* positions,
+                                   const double* inv_freq, void* q_out, void* k_pages, void* v_pages, int B, int h_q,
+                                   int h_kv, int s_q, int d_h, int d_rot, int page_size, int max_pages, int num_pages,
+                                   int interleaved, float amplitude, lka_dtype_t dtype, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    if (!rope_pages_ok(block_table, B, page_size, max_pages, num_pages)) return LKA_ERR_INVALID_ARG;
+    CacheDesc c{};
+    c.kc = k_pages;
+    c.vc = v_pages;
+    c.slab = (long long)h_kv * page_size * d_h;
+    c.k_head = c.v_head = (long long)page_size * d_h;
+    c.row = c.dv = d_h;
+    c.table = block_table;
+    c.page_size = page_size;
+    c.max_pages = max_pages;
+    c.num_pages = num_pages;
+    return append_run(q, k, v, strides, cache_lens, positions, inv_freq, q_out, B,
+                      h_q, h_kv, s_q, d_h, d_rot, page_size * max_pages, interleaved, amplitude, dtype, c, ws,
+                      ws_bytes, stream);
+}
+
+lka_status_t gqa_rope_append_fp8kv(const void* q, const void* k, const void* v, const int64_t* strides,
+                                   const float* k_scale, const float* v_scale, const int32_t* cache_lens,
+                                   const int32_t* positions, const double* inv_freq, void* q_out, void* k_cache,
+                                   void* v_cache, int B, int h_q, int h_kv, int s_q, int d_h, int d_rot, int Lmax,
+                                   int interleaved, float amplitude, void* ws, size_t ws_bytes, void* stream) {
+    CacheDesc c{};
+    c.kc = k_cache;
+    c.vc = v_cache;
+    c.slab = (long long)h_kv * Lmax * d_h;
+    c.k_head = c.v_head = (long long)Lmax * d_h;
+    c.row = c.dv = d_h;
+    c.fp8 = true;
+    c.k_scale = k_scale;
+    c.v_scale = v_scale;
+    c.scale_by_head = 1;
+    return append_run(q, k, v, strides, cache_lens, positions, inv_freq, q_out, B,
+                      h_q, h_kv, s_q, d_h, d_rot, Lmax, interleaved, amplitude, LKA_BF16, c, ws, ws_bytes, stream);
+}
+
+lka_status_t latent_rope_append(const void* q_r, const void* c_kv, const void* k_r, const int64_t* strides,
+                                const int32_t* cache_lens, const int32_t* positions, const double* inv_freq,
+                                void* q_out, void* latent, int B, int h_q, int s_q, int r_kv, int d_r, int Lmax,
+                                int interleaved, float amplitude, lka_dtype_t dtype, void* ws, size_t ws_bytes,
+                                void* stream) {
+    if (r_kv < 1 || d_r < 1) return LKA_ERR_INVALID_ARG;
+    const int eb = dtype == LKA_FP32 ? 4 : 2;
+    CacheDesc c{};
+    c.vc = latent;
+    c.kc = latent ? static_cast<uint8_t*>(latent) + (size_t)r_kv * eb : nullptr;
+    c.row = (long long)r_kv + d_r;
+    c.slab = (long long)Lmax * c.row;
+    c.dv = r_kv;
+    return append_run(q_r, k_r, c_kv, strides, cache_lens, positions, inv_freq,
+                      q_out, B, h_q, 1, s_q, d_r, d_r, Lmax, interleaved, amplitude, dtype, c, ws, ws_bytes, stream);
+}
+
+lka_status_t latent_rope_append_paged(const void* q_r, const void* c_kv, const void* k_r, const int64_t* strides,
+                                      const int32_t* block_table, const int32_t* cache_lens, const int32_t* positions,
+                                      const double* inv_freq, void* q_out, void* latent_pages, int B, int h_q, int s_q,
+                                      int r_kv, int d_r, int page_size, int max_pages, int num_pages, int interleaved,
+                                      float amplitude, lka_dtype_t dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (r_kv < 1 || d_r < 1 || !rope_pages_ok(block_table, B, page_size, max_pages, num_pages))
+        return LKA_ERR_INVALID_ARG;
+    const int eb = dtype == LKA_FP32 ? 4 : 2;
+    CacheDesc c{};
+    c.vc = latent_pages;
+    c.kc = latent_pages ? static_cast<uint8_t*>(latent_pages) + (size_t)r_kv * eb : nullptr;
+    c.row = (long long)r_kv + d_r;
+    c.slab = (long long)page_size * c.row;
+    c.dv = r_kv;
+    c.table = block_table;
+    c.page_size = page_size;
+    c.max_pages = max_pages;
+    c.num_pages = num_pages;
+    return append_run(q_r, k_r, c_kv, strides, cache_lens, positions, inv_freq,
+                      q_out, B, h_q, 1, s_q, d_r, d_r, page_size * max_pages, interleaved, amplitude, dtype, c, ws,
+                      ws_bytes, stream);
+}
+
+lka_status_t latent_rope_append_fp8kv(const void* q_r, const void* c_kv, const void* k_r, const int64_t* strides,
+                                      const float* kv_scale, const int32_t* cache_lens, const int32_t* positions,
+                                      const double* inv_freq, void* q_out, void* latent, int B, int h_q, int s_q,
+                                      int r_kv, int d_r, int Lmax, int interleaved, float amplitude, void* ws,
+                                      size_t ws_bytes, void* stream) {
+    if (r_kv < 1 || d_r < 1) return LKA_ERR_INVALID_ARG;
+    CacheDesc c{};
+    c.vc = latent;
+    c.kc = latent ? static_cast<uint8_t*>(latent) + r_kv : nullptr;
+    c.row = (long long)r_kv + d_r;
+    c.slab = (long long)Lmax * c.row;
+    c.dv = r_kv;
+    c.fp8 = true;
+    c.v_scale = kv_scale;
+    c.k_scale = kv_scale ? kv_scale + 1 : nullptr;
+    return append_run(q_r, k_r, c_kv, strides, cache_lens, positions, inv_freq,
+                      q_out, B, h_q, 1, s_q, d_r, d_r, Lmax, interleaved, amplitude, LKA_BF16, c, ws, ws_bytes,
+                      stream);
+}
+
+}  // extern "C"
