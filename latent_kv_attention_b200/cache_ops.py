@@ -11,14 +11,13 @@ can replay at the same time.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import threading
 
 import torch
 
-from . import (_check, _device_tensor, _dtype_code, _lens_tensor, _ptr, _require, library, workspaces)
+from . import _DT, _check, library, workspaces
 
 _E4M3 = torch.float8_e4m3fn
 _CACHE_DT = {torch.bfloat16: 0, torch.float32: 1, _E4M3: 2}
@@ -39,55 +38,98 @@ def captured_status(device, create=False):
         return t
 
 
-@contextlib.contextmanager
-def _on(device):
-    """The device's current stream (as a pointer) and whether it is being captured, with the device made current."""
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream()
-        yield ctypes.c_void_p(s.cuda_stream), torch.cuda.is_current_stream_capturing()
-    else:
-        with torch.cuda.device(device):
-            s = torch.cuda.current_stream()
-            yield ctypes.c_void_p(s.cuda_stream), torch.cuda.is_current_stream_capturing()
+# The checks below run on every call, a decode step's included: they compare first and word the message only when
+# something is wrong.
+def _require(cond, msg):
+    if not cond:
+        raise ValueError(msg)
 
 
-def _header(device, capturing):
-    return captured_status(device, create=True) if capturing else workspaces.get(_HEADER, device)
-
-
-def _strided(t, name, dtype, device=None):
-    _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4, f"{name} must be a 4-D CUDA tensor")
-    _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _require(t.stride(3) == 1 or t.shape[3] == 1, f"the last dimension of {name} must be contiguous")
-    _require(device is None or t.device == device, f"{name} must be on {device}")
+def _code(t, name):
+    """(device, dtype code) of the tensor that sets both for a call."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _DT.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
+    return t.device, code
 
 
 def _dense(t, name, dtype, device, shape=None):
-    _device_tensor(t, name, dtype)
-    _require(t.device == device, f"{name} must be on {device}")
-    _require(shape is None or tuple(t.shape) == tuple(shape), f"{name} must have shape {list(shape or ())}")
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous() and
+            (shape is None or t.shape == shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}" +
+                         (f" of shape {list(shape)}" if shape is not None else ""))
+    return t.data_ptr()
 
 
-def _strides(*ts):
-    return (ctypes.c_int64 * (3 * len(ts)))(*[s for t in ts for s in t.stride()[:3]])
+def _strided(t, name, dtype, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.dim() == 4):
+        raise ValueError(f"{name} must be a 4-D {dtype} tensor on {device}")
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return st
 
 
-def _frequencies(inv_freq, device):
-    _dense(inv_freq, "inv_freq", torch.float64, device)
-    return 2 * inv_freq.numel()
+def _lens(cache_lens, B, device):
+    return _dense(cache_lens, "cache_lens", torch.int32, device, (B,))
 
 
 def _positions(positions, B, s, device):
-    if positions is not None:
-        _dense(positions, "positions", torch.int32, device, (B, s))
-    return positions
+    return None if positions is None else _dense(positions, "positions", torch.int32, device, (B, s))
 
 
 def _table(block_table, B, device):
-    _dense(block_table, "block_table", torch.int32, device)
+    p = _dense(block_table, "block_table", torch.int32, device)
     _require(block_table.dim() == 2 and block_table.shape[0] == B and block_table.shape[1] >= 1,
              "block_table must be int32 [B, max_pages]")
-    return block_table.shape[1]
+    return p, block_table.shape[1]
+
+
+_I3, _I9 = ctypes.c_int64 * 3, ctypes.c_int64 * 9
+_functions = {}
+
+
+def _function(name):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(library(), name)
+    return f
+
+
+def _call(name, device, args, scratch=_HEADER):
+    """Calls the library on the device's current stream, with a workspace of `scratch` bytes after `args` (none if
+    scratch is 0).  A captured call gets its scratch from the graph's memory."""
+    f, index = _function(name), device.index
+    before = torch._C._cuda_getDevice()
+    if before != index:
+        torch.cuda.set_device(index)
+    try:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+        if scratch == 0:
+            rc = f(*args, stream)
+        elif not torch.cuda.is_current_stream_capturing():
+            if index not in _captured:
+                captured_status(device, create=True)  # outside a graph, so that no replay clears it
+            ws = workspaces._ws.get((index, stream))
+            if ws is None or ws.numel() < scratch:
+                ws = workspaces.get(scratch, device)
+            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+        elif scratch <= _HEADER:
+            ws = captured_status(device, create=True)
+            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+        else:
+            ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+            ws[:_HEADER].zero_()
+            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+            # the captured call's flags outlive its scratch
+            captured_status(device, create=True)[:4].view(torch.int32).bitwise_or_(ws[:4].view(torch.int32))
+    finally:
+        if before != index:
+            torch.cuda.set_device(before)
+    if rc:
+        _check(name, rc)
 
 
 def rope_inv_freq(d_rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -128,46 +170,58 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     views allowed), positions int32 [B,s], inv_freq fp64 radians per token.  Pairs (i, i + n), or (2i, 2i + 1) if
     interleaved.  backward=True applies the transpose: the gradient of x from the gradient of the result.
     out: a contiguous tensor of x's shape, or x itself (in place)."""
-    code = _dtype_code(x)
-    _strided(x, "x", x.dtype)
-    B, h, s, d = x.shape
-    dev = x.device
-    d_rot = _frequencies(inv_freq, dev)
-    _dense(positions, "positions", torch.int32, dev, (B, s))
+    dev, code = _code(x, "x")
+    xs = _strided(x, "x", x.dtype, dev)
+    shape = B, h, s, d = x.shape
+    freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
+    pos = _dense(positions, "positions", torch.int32, dev, (B, s))
     if out is None:
-        out = torch.empty((B, h, s, d), dtype=x.dtype, device=dev)
-    elif out.data_ptr() != x.data_ptr() or out.stride() != x.stride():
-        _dense(out, "out", x.dtype, dev, x.shape)
-        span = 1 + sum((n - 1) * abs(st) for n, st in zip(x.shape, x.stride())) if x.numel() else 0
-        e = x.element_size()
-        _require(out.data_ptr() >= x.data_ptr() + span * e or x.data_ptr() >= out.data_ptr() + out.numel() * e,
-                 "out must be x itself or share no memory with it")
-    else:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    elif out is x or (out.data_ptr() == x.data_ptr() and out.stride() == xs):
         _strided(out, "out", x.dtype, dev)
-        _require(out.shape == x.shape, "out must have x's shape")
-        _require(all(st != 0 or n == 1 for n, st in zip(x.shape, x.stride())), "in place needs x without repeated rows")
-    with _on(dev) as (stream, _):
-        rc = library().rope_apply(_ptr(x), _strides(x), _ptr(positions), _ptr(inv_freq), _ptr(out), _strides(out), B,
-                                  h, s, d, d_rot, int(bool(interleaved)), int(bool(backward)), float(amplitude), code,
-                                  stream)
-    _check("rope_apply", rc)
+        _require(out.shape == shape, "out must have x's shape")
+        _require(all(st != 0 or n == 1 for n, st in zip(shape, xs)), "in place needs x without repeated rows")
+    else:
+        at, e = _dense(out, "out", x.dtype, dev, shape), x.element_size()
+        span = 1 + sum((n - 1) * st for n, st in zip(shape, xs)) if x.numel() else 0
+        _require(at >= x.data_ptr() + span * e or x.data_ptr() >= at + out.numel() * e,
+                 "out must be x itself or share no memory with it")
+    os = out.stride()
+    _call("rope_apply", dev, (x.data_ptr(), _I3(xs[0], xs[1], xs[2]), pos, freq, out.data_ptr(),
+                              _I3(os[0], os[1], os[2]), B, h, s, d, 2 * inv_freq.numel(), bool(interleaved),
+                              bool(backward), amplitude, code), scratch=0)
     return out
 
 
 def _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out):
-    _strided(q, "q", q.dtype)
-    dev = q.device
-    B, h_q, s, d = q.shape
-    _strided(k, "k", q.dtype, dev)
-    _strided(v, "v", q.dtype, dev)
-    _require(k.shape[0] == B and k.shape[2:] == (s, d) and v.shape == k.shape, "q [B,h_q,s,d], k and v [B,h_kv,s,d]")
-    _lens_tensor(cache_lens, B, dev)
-    _positions(positions, B, s, dev)
+    """The checked operands of an append: sizes, and the arguments up to q_out."""
+    dev, code = _code(q, "q")
+    dt = q.dtype
+    qs = _strided(q, "q", dt, dev)
+    shape = B, h_q, s, d = q.shape
+    ks, vs = _strided(k, "k", dt, dev), _strided(v, "v", dt, dev)
+    h_kv = k.shape[1]
+    if k.shape != (B, h_kv, s, d) or v.shape != k.shape:
+        raise ValueError("q [B,h_q,s,d], k and v [B,h_kv,s,d]")
     if q_out is None:
-        q_out = torch.empty((B, h_q, s, d), dtype=q.dtype, device=dev)
+        q_out = torch.empty(shape, dtype=dt, device=dev)
     else:
-        _dense(q_out, "q_out", q.dtype, dev, q.shape)
-    return dev, B, h_q, k.shape[1], s, d, _frequencies(inv_freq, dev), q_out
+        _dense(q_out, "q_out", dt, dev, shape)
+    freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
+    return (dev, code, B, h_q, h_kv, s, d, q_out, _lens(cache_lens, B, dev), _positions(positions, B, s, dev), freq,
+            2 * inv_freq.numel(), (q.data_ptr(), k.data_ptr(), v.data_ptr(), _I9(*qs[:3], *ks[:3], *vs[:3])))
+
+
+def _cache_shape(cache, B, h_kv, d):
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 4:
+        raise ValueError("caches must be [B,h_kv,Lmax,d]")
+    return (B, h_kv, cache.shape[2], d)
+
+
+def _pages_shape(pages, h_kv, d, name="k_pages/v_pages"):
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 4:
+        raise ValueError(f"{name} must be [num_pages,h_kv,page_size,d]")
+    return (pages.shape[0], h_kv, pages.shape[2], d)
 
 
 def gqa_rope_append(q, k, v, k_cache, v_cache, cache_lens, inv_freq, positions=None, interleaved: bool = False,
@@ -176,18 +230,12 @@ def gqa_rope_append(q, k, v, k_cache, v_cache, cache_lens, inv_freq, positions=N
     [B,h_kv,s,d] (strided views allowed); token t is written at row cache_lens[b] - s + t of k_cache, v_cache
     [B,h_kv,Lmax,d], and stands at that position unless positions int32 [B,s] says otherwise.  Tokens before row 0
     are padding (not written, their query 0).  Returns the rotated queries [B,h_q,s,d] for gqa_attn."""
-    code = _dtype_code(q)
-    dev, B, h_q, h_kv, s, d, d_rot, q_out = _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out)
-    _dense(k_cache, "k_cache", q.dtype, dev)
-    _require(k_cache.dim() == 4 and k_cache.shape[:2] == (B, h_kv) and k_cache.shape[3] == d, "caches [B,h_kv,Lmax,d]")
-    _dense(v_cache, "v_cache", q.dtype, dev, k_cache.shape)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_rope_append(_ptr(q), _ptr(k), _ptr(v), _strides(q, k, v), _ptr(cache_lens), _ptr(positions),
-                                       _ptr(inv_freq), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), B, h_q, h_kv, s, d,
-                                       d_rot, k_cache.shape[2], int(bool(interleaved)), float(amplitude), code,
-                                       _ptr(ws), ws.numel(), stream)
-    _check("gqa_rope_append", rc)
+    dev, code, B, h_q, h_kv, s, d, q_out, lens, pos, freq, d_rot, qkv = _append_operands(
+        q, k, v, cache_lens, inv_freq, positions, q_out)
+    shape = _cache_shape(k_cache, B, h_kv, d)
+    kc, vc = _dense(k_cache, "k_cache", q.dtype, dev, shape), _dense(v_cache, "v_cache", q.dtype, dev, shape)
+    _call("gqa_rope_append", dev, (*qkv, lens, pos, freq, q_out.data_ptr(), kc, vc, B, h_q, h_kv, s, d, d_rot, shape[2],
+                                   bool(interleaved), amplitude, code))
     return q_out
 
 
@@ -195,21 +243,13 @@ def gqa_rope_append_paged(q, k, v, k_pages, v_pages, block_table, cache_lens, in
                           interleaved: bool = False, amplitude: float = 1.0, q_out=None):
     """gqa_rope_append into paged caches: k_pages, v_pages [num_pages,h_kv,page_size,d], block_table int32
     [B,max_pages].  A token whose page is outside the pool is not written (reported in device_status)."""
-    code = _dtype_code(q)
-    dev, B, h_q, h_kv, s, d, d_rot, q_out = _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out)
-    _dense(k_pages, "k_pages", q.dtype, dev)
-    _require(k_pages.dim() == 4 and k_pages.shape[1] == h_kv and k_pages.shape[3] == d,
-             "k_pages/v_pages [num_pages,h_kv,page_size,d]")
-    _dense(v_pages, "v_pages", q.dtype, dev, k_pages.shape)
-    max_pages = _table(block_table, B, dev)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_rope_append_paged(_ptr(q), _ptr(k), _ptr(v), _strides(q, k, v), _ptr(block_table),
-                                             _ptr(cache_lens), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
-                                             _ptr(k_pages), _ptr(v_pages), B, h_q, h_kv, s, d, d_rot, k_pages.shape[2],
-                                             max_pages, k_pages.shape[0], int(bool(interleaved)), float(amplitude),
-                                             code, _ptr(ws), ws.numel(), stream)
-    _check("gqa_rope_append_paged", rc)
+    dev, code, B, h_q, h_kv, s, d, q_out, lens, pos, freq, d_rot, qkv = _append_operands(
+        q, k, v, cache_lens, inv_freq, positions, q_out)
+    shape = _pages_shape(k_pages, h_kv, d)
+    kc, vc = _dense(k_pages, "k_pages", q.dtype, dev, shape), _dense(v_pages, "v_pages", q.dtype, dev, shape)
+    table, max_pages = _table(block_table, B, dev)
+    _call("gqa_rope_append_paged", dev, (*qkv, table, lens, pos, freq, q_out.data_ptr(), kc, vc, B, h_q, h_kv, s, d,
+                                         d_rot, shape[2], max_pages, shape[0], bool(interleaved), amplitude, code))
     return q_out
 
 
@@ -218,75 +258,64 @@ def gqa_rope_append_fp8kv(q, k, v, k_cache, v_cache, k_scale, v_scale, cache_len
     """gqa_rope_append into e4m3 caches (torch.float8_e4m3fn) with fp32 scales [h_kv]: the caches hold key / k_scale
     and value / v_scale, rounded to nearest even and saturated.  q, k, v bf16."""
     _require(isinstance(q, torch.Tensor) and q.dtype == torch.bfloat16, "q must be torch.bfloat16")
-    dev, B, h_q, h_kv, s, d, d_rot, q_out = _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out)
-    _dense(k_cache, "k_cache", _E4M3, dev)
-    _require(k_cache.dim() == 4 and k_cache.shape[:2] == (B, h_kv) and k_cache.shape[3] == d, "caches [B,h_kv,Lmax,d]")
-    _dense(v_cache, "v_cache", _E4M3, dev, k_cache.shape)
-    _dense(k_scale, "k_scale", torch.float32, dev, (h_kv,))
-    _dense(v_scale, "v_scale", torch.float32, dev, (h_kv,))
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_rope_append_fp8kv(_ptr(q), _ptr(k), _ptr(v), _strides(q, k, v), _ptr(k_scale),
-                                             _ptr(v_scale), _ptr(cache_lens), _ptr(positions), _ptr(inv_freq),
-                                             _ptr(q_out), _ptr(k_cache), _ptr(v_cache), B, h_q, h_kv, s, d, d_rot,
-                                             k_cache.shape[2], int(bool(interleaved)), float(amplitude), _ptr(ws),
-                                             ws.numel(), stream)
-    _check("gqa_rope_append_fp8kv", rc)
+    dev, _, B, h_q, h_kv, s, d, q_out, lens, pos, freq, d_rot, qkv = _append_operands(
+        q, k, v, cache_lens, inv_freq, positions, q_out)
+    shape = _cache_shape(k_cache, B, h_kv, d)
+    kc, vc = _dense(k_cache, "k_cache", _E4M3, dev, shape), _dense(v_cache, "v_cache", _E4M3, dev, shape)
+    ks = _dense(k_scale, "k_scale", torch.float32, dev, (h_kv,))
+    vs = _dense(v_scale, "v_scale", torch.float32, dev, (h_kv,))
+    _call("gqa_rope_append_fp8kv", dev, (*qkv, ks, vs, lens, pos, freq, q_out.data_ptr(), kc, vc, B, h_q, h_kv, s, d,
+                                         d_rot, shape[2], bool(interleaved), amplitude))
     return q_out
 
 
 def _latent_operands(q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out):
-    _strided(q_r, "q_r", q_r.dtype)
-    dev = q_r.device
-    B, h_q, s, d_r = q_r.shape
-    _strided(c_kv, "c_kv", q_r.dtype, dev)
-    _strided(k_r, "k_r", q_r.dtype, dev)
-    _require(c_kv.shape[:3] == (B, 1, s) and k_r.shape == (B, 1, s, d_r), "q_r [B,h_q,s,d_r], c_kv [B,1,s,r_kv], k_r [B,1,s,d_r]")
-    _lens_tensor(cache_lens, B, dev)
-    _positions(positions, B, s, dev)
-    _require(_frequencies(inv_freq, dev) == d_r, "inv_freq must hold d_r / 2 values")
+    dev, code = _code(q_r, "q_r")
+    dt = q_r.dtype
+    qs = _strided(q_r, "q_r", dt, dev)
+    shape = B, h_q, s, d_r = q_r.shape
+    cs, ks = _strided(c_kv, "c_kv", dt, dev), _strided(k_r, "k_r", dt, dev)
+    _require(c_kv.shape[:3] == (B, 1, s) and k_r.shape == (B, 1, s, d_r),
+             "q_r [B,h_q,s,d_r], c_kv [B,1,s,r_kv], k_r [B,1,s,d_r]")
+    freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
+    _require(2 * inv_freq.numel() == d_r, "inv_freq must hold d_r / 2 values")
     if q_out is None:
-        q_out = torch.empty((B, h_q, s, d_r), dtype=q_r.dtype, device=dev)
+        q_out = torch.empty(shape, dtype=dt, device=dev)
     else:
-        _dense(q_out, "q_out", q_r.dtype, dev, q_r.shape)
-    return dev, B, h_q, s, c_kv.shape[3], d_r, q_out
+        _dense(q_out, "q_out", dt, dev, shape)
+    return (dev, code, B, h_q, s, c_kv.shape[3], d_r, q_out, _lens(cache_lens, B, dev),
+            _positions(positions, B, s, dev), freq,
+            (q_r.data_ptr(), c_kv.data_ptr(), k_r.data_ptr(), _I9(*qs[:3], *ks[:3], *cs[:3])))
+
+
+def _latent_rows(t, name, n0, width):
+    _require(isinstance(t, torch.Tensor) and t.dim() == 3, f"{name} must be 3-D")
+    return (t.shape[0] if n0 is None else n0, t.shape[1], width)
 
 
 def latent_rope_append(q_r, c_kv, k_r, latent, cache_lens, inv_freq, positions=None, interleaved: bool = False,
                        amplitude: float = 1.0, q_out=None):
     """The latent cache's append: q_r [B,h_q,s,d_r] and k_r [B,1,s,d_r] are rotated, and [c_kv ; k_r] (c_kv
     [B,1,s,r_kv]) is written to rows cache_lens[b] - s + t of latent [B,Lmax,r_kv+d_r].  Returns the rotated q_r."""
-    code = _dtype_code(q_r)
-    dev, B, h_q, s, r_kv, d_r, q_out = _latent_operands(q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out)
-    _dense(latent, "latent", q_r.dtype, dev)
-    _require(latent.dim() == 3 and latent.shape[0] == B and latent.shape[2] == r_kv + d_r, "latent [B,Lmax,r_kv+d_r]")
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().latent_rope_append(_ptr(q_r), _ptr(c_kv), _ptr(k_r), _strides(q_r, k_r, c_kv), _ptr(cache_lens),
-                                          _ptr(positions), _ptr(inv_freq), _ptr(q_out), _ptr(latent), B, h_q, s, r_kv,
-                                          d_r, latent.shape[1], int(bool(interleaved)), float(amplitude), code,
-                                          _ptr(ws), ws.numel(), stream)
-    _check("latent_rope_append", rc)
+    dev, code, B, h_q, s, r_kv, d_r, q_out, lens, pos, freq, qck = _latent_operands(
+        q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out)
+    shape = _latent_rows(latent, "latent", B, r_kv + d_r)
+    cache = _dense(latent, "latent", q_r.dtype, dev, shape)
+    _call("latent_rope_append", dev, (*qck, lens, pos, freq, q_out.data_ptr(), cache, B, h_q, s, r_kv, d_r, shape[1],
+                                      bool(interleaved), amplitude, code))
     return q_out
 
 
 def latent_rope_append_paged(q_r, c_kv, k_r, latent_pages, block_table, cache_lens, inv_freq, positions=None,
                              interleaved: bool = False, amplitude: float = 1.0, q_out=None):
     """latent_rope_append into a paged latent cache [num_pages,page_size,r_kv+d_r] through block_table."""
-    code = _dtype_code(q_r)
-    dev, B, h_q, s, r_kv, d_r, q_out = _latent_operands(q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out)
-    _dense(latent_pages, "latent_pages", q_r.dtype, dev)
-    _require(latent_pages.dim() == 3 and latent_pages.shape[2] == r_kv + d_r, "latent_pages [num_pages,page_size,r_kv+d_r]")
-    max_pages = _table(block_table, B, dev)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().latent_rope_append_paged(_ptr(q_r), _ptr(c_kv), _ptr(k_r), _strides(q_r, k_r, c_kv),
-                                                _ptr(block_table), _ptr(cache_lens), _ptr(positions), _ptr(inv_freq),
-                                                _ptr(q_out), _ptr(latent_pages), B, h_q, s, r_kv, d_r,
-                                                latent_pages.shape[1], max_pages, latent_pages.shape[0],
-                                                int(bool(interleaved)), float(amplitude), code, _ptr(ws), ws.numel(),
-                                                stream)
-    _check("latent_rope_append_paged", rc)
+    dev, code, B, h_q, s, r_kv, d_r, q_out, lens, pos, freq, qck = _latent_operands(
+        q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out)
+    shape = _latent_rows(latent_pages, "latent_pages", None, r_kv + d_r)
+    cache = _dense(latent_pages, "latent_pages", q_r.dtype, dev, shape)
+    table, max_pages = _table(block_table, B, dev)
+    _call("latent_rope_append_paged", dev, (*qck, table, lens, pos, freq, q_out.data_ptr(), cache, B, h_q, s, r_kv, d_r,
+                                            shape[1], max_pages, shape[0], bool(interleaved), amplitude, code))
     return q_out
 
 
@@ -294,48 +323,32 @@ def latent_rope_append_fp8kv(q_r, c_kv, k_r, latent, kv_scale, cache_lens, inv_f
                              interleaved: bool = False, amplitude: float = 1.0, q_out=None):
     """latent_rope_append into an e4m3 latent cache with kv_scale fp32 [2]: c_kv / kv_scale[0], k_r / kv_scale[1]."""
     _require(isinstance(q_r, torch.Tensor) and q_r.dtype == torch.bfloat16, "q_r must be torch.bfloat16")
-    dev, B, h_q, s, r_kv, d_r, q_out = _latent_operands(q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out)
-    _dense(latent, "latent", _E4M3, dev)
-    _require(latent.dim() == 3 and latent.shape[0] == B and latent.shape[2] == r_kv + d_r, "latent [B,Lmax,r_kv+d_r]")
-    _dense(kv_scale, "kv_scale", torch.float32, dev, (2,))
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().latent_rope_append_fp8kv(_ptr(q_r), _ptr(c_kv), _ptr(k_r), _strides(q_r, k_r, c_kv),
-                                                _ptr(kv_scale), _ptr(cache_lens), _ptr(positions), _ptr(inv_freq),
-                                                _ptr(q_out), _ptr(latent), B, h_q, s, r_kv, d_r, latent.shape[1],
-                                                int(bool(interleaved)), float(amplitude), _ptr(ws), ws.numel(), stream)
-    _check("latent_rope_append_fp8kv", rc)
+    dev, _, B, h_q, s, r_kv, d_r, q_out, lens, pos, freq, qck = _latent_operands(
+        q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out)
+    shape = _latent_rows(latent, "latent", B, r_kv + d_r)
+    cache = _dense(latent, "latent", _E4M3, dev, shape)
+    sc = _dense(kv_scale, "kv_scale", torch.float32, dev, (2,))
+    _call("latent_rope_append_fp8kv", dev, (*qck, sc, lens, pos, freq, q_out.data_ptr(), cache, B, h_q, s, r_kv, d_r,
+                                            shape[1], bool(interleaved), amplitude))
     return q_out
 
 
-def _attn_outputs(q, scale, out, return_lse):
+def _attn_outputs(q, out, return_lse):
     B, h_q, s, d = q.shape
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
         _dense(out, "out", q.dtype, q.device, q.shape)
     lse = torch.empty((B, h_q, s), dtype=torch.float32, device=q.device) if return_lse else None
-    return scale, out, lse
+    return out, lse, lse.data_ptr() if return_lse else None
 
 
-def _prefix_scratch(nbytes, dev, capturing):
-    if not capturing:
-        return workspaces.get(nbytes, dev)
-    ws = torch.empty(max(nbytes, _HEADER), dtype=torch.uint8, device=dev)
-    ws[:_HEADER].zero_()
-    return ws
-
-
-def _prefix_done(ws, dev, capturing):
-    if capturing:  # the captured call's flags outlive its scratch
-        captured_status(dev, create=True)[:4].view(torch.int32).bitwise_or_(ws[:4].view(torch.int32))
+def _scale(scale, d):
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
 
 def _prefix_len(prefix_len, device):
-    if prefix_len is not None:
-        _dense(prefix_len, "prefix_len", torch.int32, device)
-        _require(prefix_len.numel() == 1, "prefix_len must be int32 [1] on the device")
+    return None if prefix_len is None else _dense(prefix_len, "prefix_len", torch.int32, device, (1,))
 
 
 def gqa_attn_shared_prefix(q, k_prefix, v_prefix, k, v, cache_lens, prefix_len=None, causal: bool = True,
@@ -344,27 +357,21 @@ def gqa_attn_shared_prefix(q, k_prefix, v_prefix, k, v, cache_lens, prefix_len=N
     (prefix_len int32 [1] on the device, or all Lp); k, v [B,h_kv,Lmax,d] with cache_lens int32 [B] the suffix
     lengths including the s_q new tokens.  Every query sees the whole prefix, then its suffix as in gqa_attn.
     Returns out [B,h_q,s_q,d] (and lse [B,h_q,s_q] fp32 over all keys if return_lse)."""
-    code = _dtype_code(q)
-    _device_tensor(q, "q", q.dtype)
-    dev = q.device
-    _require(q.dim() == 4 and k.dim() == 4 and k_prefix.dim() == 3, "q [B,h_q,s_q,d], k/v [B,h_kv,Lmax,d], prefix [h_kv,Lp,d]")
+    dev, code = _code(q, "q")
+    dt = q.dtype
+    qp = _dense(q, "q", dt, dev)
+    if q.dim() != 4 or k.dim() != 4 or k_prefix.dim() != 3:
+        raise ValueError("q [B,h_q,s_q,d], k/v [B,h_kv,Lmax,d], prefix [h_kv,Lp,d]")
     B, h_q, s, d = q.shape
     h_kv, Lmax, Lp = k.shape[1], k.shape[2], k_prefix.shape[1]
-    _dense(k, "k", q.dtype, dev, (B, h_kv, Lmax, d))
-    _dense(v, "v", q.dtype, dev, k.shape)
-    _dense(k_prefix, "k_prefix", q.dtype, dev, (h_kv, Lp, d))
-    _dense(v_prefix, "v_prefix", q.dtype, dev, k_prefix.shape)
-    _lens_tensor(cache_lens, B, dev)
-    _prefix_len(prefix_len, dev)
-    scale, out, lse = _attn_outputs(q, scale, out, return_lse)
-    lib = library()
-    with _on(dev) as (stream, capturing):
-        ws = _prefix_scratch(lib.gqa_attn_shared_prefix_workspace_size(B, h_q, h_kv, s, d, Lp, Lmax, code), dev, capturing)
-        rc = lib.gqa_attn_shared_prefix(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), _ptr(k), _ptr(v),
-                                        _ptr(cache_lens), _ptr(out), _ptr(lse), B, h_q, h_kv, s, d, Lp, Lmax,
-                                        int(bool(causal)), scale, code, _ptr(ws), ws.numel(), stream)
-        _check("gqa_attn_shared_prefix", rc)
-        _prefix_done(ws, dev, capturing)
+    own, shared = (B, h_kv, Lmax, d), (h_kv, Lp, d)
+    kp, vp = _dense(k_prefix, "k_prefix", dt, dev, shared), _dense(v_prefix, "v_prefix", dt, dev, shared)
+    ko, vo = _dense(k, "k", dt, dev, own), _dense(v, "v", dt, dev, own)
+    lens, plen = _lens(cache_lens, B, dev), _prefix_len(prefix_len, dev)
+    out, lse, lp = _attn_outputs(q, out, return_lse)
+    n = _function("gqa_attn_shared_prefix_workspace_size")(B, h_q, h_kv, s, d, Lp, Lmax, code)
+    _call("gqa_attn_shared_prefix", dev, (qp, kp, vp, plen, ko, vo, lens, out.data_ptr(), lp, B, h_q, h_kv, s, d, Lp,
+                                          Lmax, bool(causal), _scale(scale, d), code), max(n, _HEADER))
     return (out, lse) if return_lse else out
 
 
@@ -373,31 +380,23 @@ def gqa_attn_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, 
     """gqa_attn_shared_prefix over one paged pool [num_pages,h_kv,page_size,d]: the prefix's pages are prefix_table
     int32 [max_prefix_pages] (prefix_len int32 [1] on the device, or None for all their rows), a sequence's suffix
     starts at row 0 of block_table[b, 0]."""
-    code = _dtype_code(q)
-    _device_tensor(q, "q", q.dtype)
-    dev = q.device
-    _require(q.dim() == 4 and k_pages.dim() == 4, "q [B,h_q,s_q,d], k_pages/v_pages [num_pages,h_kv,page_size,d]")
+    dev, code = _code(q, "q")
+    dt = q.dtype
+    qp = _dense(q, "q", dt, dev)
+    _require(q.dim() == 4, "q [B,h_q,s_q,d]")
     B, h_q, s, d = q.shape
-    num_pages, h_kv, page_size, dk = k_pages.shape
-    _require(dk == d, "q and the pages disagree on d")
-    _dense(k_pages, "k_pages", q.dtype, dev)
-    _dense(v_pages, "v_pages", q.dtype, dev, k_pages.shape)
-    _dense(prefix_table, "prefix_table", torch.int32, dev)
+    _require(isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4, "k_pages/v_pages [num_pages,h_kv,page_size,d]")
+    num_pages, h_kv, page_size, _ = shape = _pages_shape(k_pages, k_pages.shape[1], d)
+    kp, vp = _dense(k_pages, "k_pages", dt, dev, shape), _dense(v_pages, "v_pages", dt, dev, shape)
+    ptab = _dense(prefix_table, "prefix_table", torch.int32, dev)
     _require(prefix_table.dim() == 1, "prefix_table must be int32 [max_prefix_pages]")
-    mp, max_pages = prefix_table.shape[0], _table(block_table, B, dev)
-    _lens_tensor(cache_lens, B, dev)
-    _prefix_len(prefix_len, dev)
-    scale, out, lse = _attn_outputs(q, scale, out, return_lse)
-    lib = library()
-    with _on(dev) as (stream, capturing):
-        nbytes = lib.gqa_attn_shared_prefix_paged_workspace_size(B, h_q, h_kv, s, d, page_size, mp, max_pages, code)
-        ws = _prefix_scratch(nbytes, dev, capturing)
-        rc = lib.gqa_attn_shared_prefix_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(prefix_table),
-                                              _ptr(prefix_len), _ptr(block_table), _ptr(cache_lens), _ptr(out),
-                                              _ptr(lse), B, h_q, h_kv, s, d, page_size, mp, max_pages, num_pages,
-                                              int(bool(causal)), scale, code, _ptr(ws), ws.numel(), stream)
-        _check("gqa_attn_shared_prefix_paged", rc)
-        _prefix_done(ws, dev, capturing)
+    mp, (table, max_pages) = prefix_table.shape[0], _table(block_table, B, dev)
+    lens, plen = _lens(cache_lens, B, dev), _prefix_len(prefix_len, dev)
+    out, lse, lp = _attn_outputs(q, out, return_lse)
+    n = _function("gqa_attn_shared_prefix_paged_workspace_size")(B, h_q, h_kv, s, d, page_size, mp, max_pages, code)
+    _call("gqa_attn_shared_prefix_paged", dev, (qp, kp, vp, ptab, plen, table, lens, out.data_ptr(), lp, B, h_q, h_kv,
+                                                s, d, page_size, mp, max_pages, num_pages, bool(causal),
+                                                _scale(scale, d), code), max(n, _HEADER))
     return (out, lse) if return_lse else out
 
 
@@ -412,23 +411,17 @@ def gqa_key_weights(q, k, lse, cache_lens, weights=None, causal: bool = True, sc
     """The attention weight each cached key received from these queries, summed over the queries and the heads of its
     group: q, k, cache_lens, causal and scale as given to gqa_attn and lse [B,h_q,s_q] as it returned it.  Returns
     weights fp32 [B,h_kv,Lmax] (0 from cache_lens on), or adds to the given `weights` and returns them."""
-    code = _dtype_code(q)
-    for n, t in (("q", q), ("k", k)):
-        _device_tensor(t, n, q.dtype)
-    dev = q.device
-    _require(q.dim() == 4 and k.dim() == 4 and k.device == dev, "q [B,h_q,s_q,d], k [B,h_kv,Lmax,d]")
+    dev, code = _code(q, "q")
+    qp = _dense(q, "q", q.dtype, dev)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [B,h_q,s_q,d], k [B,h_kv,Lmax,d]")
     B, h_q, s, d = q.shape
-    _, h_kv, Lmax, dk = k.shape
-    _require(dk == d and k.shape[0] == B, "q and k disagree on B or d")
-    _dense(lse, "lse", torch.float32, dev, (B, h_q, s))
-    _lens_tensor(cache_lens, B, dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    weights, add = _weights_out(weights, (B, h_kv, Lmax), dev)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(cache_lens), _ptr(weights), B, h_q, h_kv, s,
-                                       d, Lmax, int(bool(causal)), add, scale, code, _ptr(ws), ws.numel(), stream)
-    _check("gqa_key_weights", rc)
+    shape = _cache_shape(k, B, k.shape[1], d)
+    kp, lp = _dense(k, "k", q.dtype, dev, shape), _dense(lse, "lse", torch.float32, dev, (B, h_q, s))
+    lens = _lens(cache_lens, B, dev)
+    weights, add = _weights_out(weights, shape[:3], dev)
+    _call("gqa_key_weights", dev, (qp, kp, lp, lens, weights.data_ptr(), B, h_q, shape[1], s, d, shape[2], bool(causal),
+                                   add, _scale(scale, d), code))
     return weights
 
 
@@ -436,26 +429,18 @@ def gqa_key_weights_paged(q, k_pages, lse, block_table, cache_lens, weights=None
                           scale: float | None = None):
     """gqa_key_weights over a paged key cache [num_pages,h_kv,page_size,d]; weights fp32 [B,h_kv,max_pages*page_size]
     in token order."""
-    code = _dtype_code(q)
-    for n, t in (("q", q), ("k_pages", k_pages)):
-        _device_tensor(t, n, q.dtype)
-    dev = q.device
-    _require(q.dim() == 4 and k_pages.dim() == 4 and k_pages.device == dev,
+    dev, code = _code(q, "q")
+    qp = _dense(q, "q", q.dtype, dev)
+    _require(q.dim() == 4 and isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4,
              "q [B,h_q,s_q,d], k_pages [num_pages,h_kv,page_size,d]")
     B, h_q, s, d = q.shape
-    num_pages, h_kv, page_size, dk = k_pages.shape
-    _require(dk == d, "q and the pages disagree on d")
-    max_pages = _table(block_table, B, dev)
-    _dense(lse, "lse", torch.float32, dev, (B, h_q, s))
-    _lens_tensor(cache_lens, B, dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    num_pages, h_kv, page_size, _ = shape = _pages_shape(k_pages, k_pages.shape[1], d, "k_pages")
+    kp, lp = _dense(k_pages, "k_pages", q.dtype, dev, shape), _dense(lse, "lse", torch.float32, dev, (B, h_q, s))
+    table, max_pages = _table(block_table, B, dev)
+    lens = _lens(cache_lens, B, dev)
     weights, add = _weights_out(weights, (B, h_kv, max_pages * page_size), dev)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_key_weights_paged(_ptr(q), _ptr(k_pages), _ptr(lse), _ptr(block_table), _ptr(cache_lens),
-                                             _ptr(weights), B, h_q, h_kv, s, d, page_size, max_pages, num_pages,
-                                             int(bool(causal)), add, scale, code, _ptr(ws), ws.numel(), stream)
-    _check("gqa_key_weights_paged", rc)
+    _call("gqa_key_weights_paged", dev, (qp, kp, lp, table, lens, weights.data_ptr(), B, h_q, h_kv, s, d, page_size,
+                                         max_pages, num_pages, bool(causal), add, _scale(scale, d), code))
     return weights
 
 
@@ -474,33 +459,27 @@ def gqa_evict(k, v, weights, cache_lens, budget: int, sinks: int = 0, recent: in
     _require(isinstance(k, torch.Tensor) and k.dtype in _CACHE_DT and k.dim() == 4,
              "k must be bf16, fp32 or e4m3 [B,h_kv,Lmax,d]")
     dev, dt = k.device, k.dtype
-    B, h_kv, Lmax, d = k.shape
+    _require(k.is_cuda, "k must be a CUDA tensor")
+    B, h_kv, Lmax, d = shape = k.shape
     budget, sinks, recent = int(budget), int(sinks), int(recent)
-    _require(budget >= 1 and sinks >= 0 and recent >= 0, "budget must be at least 1, sinks and recent at least 0")
-    _dense(k, "k", dt, dev)
-    _dense(v, "v", dt, dev, k.shape)
-    _dense(weights, "weights", torch.float32, dev, (B, h_kv, Lmax))
-    _lens_tensor(cache_lens, B, dev)
+    if budget < 1 or sinks < 0 or recent < 0:
+        raise ValueError("budget must be at least 1, sinks and recent at least 0")
+    kp, vp = _dense(k, "k", dt, dev, shape), _dense(v, "v", dt, dev, shape)
+    wp, lens = _dense(weights, "weights", torch.float32, dev, (B, h_kv, Lmax)), _lens(cache_lens, B, dev)
     _require((k_out is None) == (v_out is None), "k_out and v_out come together")
     if k_out is None:
         k_out, v_out = (torch.zeros((B, h_kv, budget, d), dtype=torch.uint8 if dt == _E4M3 else dt, device=dev).view(dt)
                         for _ in range(2))
-    _dense(k_out, "k_out", dt, dev)
-    _require(k_out.dim() == 4 and k_out.shape[:2] == (B, h_kv) and k_out.shape[3] == d, "k_out [B,h_kv,Lout,d]")
-    Lout = k_out.shape[2]
-    _require(Lout >= budget, "k_out holds fewer rows than the budget")
-    _dense(v_out, "v_out", dt, dev, k_out.shape)
+    to = _cache_shape(k_out, B, h_kv, d)
+    ko, vo = _dense(k_out, "k_out", dt, dev, to), _dense(v_out, "v_out", dt, dev, to)
+    _require(to[2] >= budget, "k_out holds fewer rows than the budget")
     if weights_out is None:
-        _require(k_out.data_ptr() != k.data_ptr() or k.numel() == 0, "in place needs weights_out=weights")
-        weights_out = torch.empty((B, h_kv, Lout), dtype=torch.float32, device=dev)
-    _dense(weights_out, "weights_out", torch.float32, dev, (B, h_kv, Lout))
+        _require(ko != kp or k.numel() == 0, "in place needs weights_out=weights")
+        weights_out = torch.empty(to[:3], dtype=torch.float32, device=dev)
+    wo = _dense(weights_out, "weights_out", torch.float32, dev, to[:3])
     new_lens, kept = _evict_outputs(B, h_kv, budget, dev)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_evict(_ptr(k), _ptr(v), _ptr(weights), _ptr(cache_lens), _ptr(k_out), _ptr(v_out),
-                                 _ptr(weights_out), _ptr(new_lens), _ptr(kept), B, h_kv, d, Lmax, Lout, budget, sinks,
-                                 recent, _CACHE_DT[dt], _ptr(ws), ws.numel(), stream)
-    _check("gqa_evict", rc)
+    _call("gqa_evict", dev, (kp, vp, wp, lens, ko, vo, wo, new_lens.data_ptr(), kept.data_ptr(), B, h_kv, d, Lmax, to[2],
+                             budget, sinks, recent, _CACHE_DT[dt]))
     return k_out, v_out, weights_out, new_lens, kept
 
 
@@ -511,22 +490,18 @@ def gqa_evict_paged(k_pages, v_pages, weights, block_table, cache_lens, budget: 
     _require(isinstance(k_pages, torch.Tensor) and k_pages.dtype in _CACHE_DT and k_pages.dim() == 4,
              "k_pages must be bf16, fp32 or e4m3 [num_pages,h_kv,page_size,d]")
     dev, dt = k_pages.device, k_pages.dtype
-    num_pages, h_kv, page_size, d = k_pages.shape
-    _dense(k_pages, "k_pages", dt, dev)
-    _dense(v_pages, "v_pages", dt, dev, k_pages.shape)
+    _require(k_pages.is_cuda, "k_pages must be a CUDA tensor")
+    num_pages, h_kv, page_size, d = shape = k_pages.shape
+    kp, vp = _dense(k_pages, "k_pages", dt, dev, shape), _dense(v_pages, "v_pages", dt, dev, shape)
     _require(isinstance(block_table, torch.Tensor) and block_table.dim() == 2, "block_table must be int32 [B, max_pages]")
     B = block_table.shape[0]
-    max_pages = _table(block_table, B, dev)
-    _dense(weights, "weights", torch.float32, dev, (B, h_kv, max_pages * page_size))
-    _lens_tensor(cache_lens, B, dev)
+    table, max_pages = _table(block_table, B, dev)
+    wp = _dense(weights, "weights", torch.float32, dev, (B, h_kv, max_pages * page_size))
+    lens = _lens(cache_lens, B, dev)
     budget, sinks, recent = int(budget), int(sinks), int(recent)
     _require(1 <= budget <= max_pages * page_size and sinks >= 0 and recent >= 0,
              "budget must be between 1 and the table's capacity, sinks and recent at least 0")
     new_lens, kept = _evict_outputs(B, h_kv, budget, dev)
-    with _on(dev) as (stream, capturing):
-        ws = _header(dev, capturing)
-        rc = library().gqa_evict_paged(_ptr(k_pages), _ptr(v_pages), _ptr(weights), _ptr(block_table),
-                                       _ptr(cache_lens), _ptr(new_lens), _ptr(kept), B, h_kv, d, page_size, max_pages,
-                                       num_pages, budget, sinks, recent, _CACHE_DT[dt], _ptr(ws), ws.numel(), stream)
-    _check("gqa_evict_paged", rc)
+    _call("gqa_evict_paged", dev, (kp, vp, wp, table, lens, new_lens.data_ptr(), kept.data_ptr(), B, h_kv, d, page_size,
+                                   max_pages, num_pages, budget, sinks, recent, _CACHE_DT[dt]))
     return new_lens, kept

@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "launch_util.h"
 #include "mma.cuh"
 
 namespace lka {
@@ -249,11 +250,10 @@ cudaError_t launch_mma(KeyWeightParams p, const dim3& grid, cudaStream_t st) {
     // whole groups of 8 rows; 64 rows at a time hide the copies of the next ones behind 8 MMA column groups
     p.chunk = std::min(64, cdiv(p.ratio * p.s, 8) * 8);
     const int smem = 2 * p.chunk * (D * 2 + 64 + 4);
-    auto kern = key_weights_mma_kernel<D>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<key_weights_mma_kernel<D>>(2 * 64 * (D * 2 + 64 + 4));
     if (e != cudaSuccess) return e;
     TimedLaunch timer(st);
-    kern<<<grid, 128, smem, st>>>(p);
+    key_weights_mma_kernel<D><<<grid, 128, smem, st>>>(p);
     timer.stop();
     return cudaPeekAtLastError();
 }
@@ -261,11 +261,10 @@ cudaError_t launch_mma(KeyWeightParams p, const dim3& grid, cudaStream_t st) {
 template <int D>
 cudaError_t launch_f32(const KeyWeightParams& p, const dim3& grid, cudaStream_t st) {
     constexpr int smem = (kTile * (D + 4) + 16 * D + 16 + kTile) * 4;
-    auto kern = key_weights_f32_kernel<D>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<key_weights_f32_kernel<D>>(smem);
     if (e != cudaSuccess) return e;
     TimedLaunch timer(st);
-    kern<<<grid, 128, smem, st>>>(p);
+    key_weights_f32_kernel<D><<<grid, 128, smem, st>>>(p);
     timer.stop();
     return cudaPeekAtLastError();
 }

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "launch_util.h"
 #include "mma.cuh"
 #include "prefix_attn.h"
 
@@ -485,6 +486,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 
 // ---- planning ------------------------------------------------------------------------------------------------------
 struct PrefixPlan {
+    bool tc;                 // the prefix runs on prefix_tc_kernel
     int rows_pre, rows_suf;  // query rows per block of the prefix and the suffix kernel
     int pre_tokens, n_pre, suf_tokens, n_suf;
     size_t off_lse, off_o, ws_bytes;
@@ -514,15 +516,21 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     if ((long long)B * h_q * s >= (1ll << 28) || Lp > (1 << 30) || Lmax > (1 << 30)) return LKA_ERR_UNSUPPORTED;
     const int R = h_q / h_kv * s, Bn = std::max(B, 1);
     const bool f32 = dtype == LKA_FP32;
-    // up to 16 rows in all, the four warps split the keys; more, they split the rows and the prefix is read once
-    // per 64 of them
+    // Up to 16 query rows per KV head in all, warps split the keys of prefix_mma_kernel.  More, and the head dim fits
+    // prefix_tc_kernel's tensor memory: that one.  d = 256: prefix_mma_kernel with the rows split over the warps, the
+    // prefix read once per 64 of them.
+    pl->tc = !f32 && Bn * R > 16 && d <= 128;
     pl->rows_pre = f32 || Bn * R <= 16 ? 16 : 64;
     pl->rows_suf = 16;
     const int tile = f32 ? 32 : 64;
     const double slots = (double)sm_count() * (f32 ? 3 : d == 256 ? 1 : 2);
     const int knob = split_tokens_knob();
-    pl->pre_tokens = knob > 0 ? cdiv(knob, tile) * tile
-                              : split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile);
+    if (pl->tc)
+        pl->pre_tokens = knob > 0 ? cdiv(knob, 128) * 128
+                                  : split_keys((double)h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), sm_count(), Lp, 128);
+    else
+        pl->pre_tokens = knob > 0 ? cdiv(knob, tile) * tile
+                                  : split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile);
     pl->suf_tokens = knob > 0 ? cdiv(knob, tile) * tile
                               : split_keys((double)h_kv * Bn * cdiv(R, pl->rows_suf), slots, Lmax, tile);
     pl->n_pre = cdiv(Lp, pl->pre_tokens);
@@ -535,30 +543,35 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     return LKA_OK;
 }
 
-template <typename K>
-cudaError_t launch_attn(K kern, int smem, const PrefixParams& p, int rows, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto KERN>
+cudaError_t launch_attn(int smem, const PrefixParams& p, int rows, cudaStream_t st) {
+    const cudaError_t e = allow_smem<KERN>(smem);
     if (e != cudaSuccess) return e;
     const long long n = (p.do_prefix ? (long long)cdiv(p.B * p.R, rows) * p.h_kv * p.n_pre : 0) +
                         (p.do_suffix ? (long long)p.B * p.h_kv * cdiv(p.R, rows) * p.n_suf : 0);
     if (n == 0) return cudaSuccess;
     if (n >= (1ll << 31)) return cudaErrorInvalidValue;
-    kern<<<(unsigned)n, 128, smem, st>>>(p);
+    KERN<<<(unsigned)n, 128, smem, st>>>(p);
     return cudaPeekAtLastError();
 }
 
 template <int D>
 cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
-    TimedLaunch timer(st);
     cudaError_t e = cudaSuccess;
-    if (pl.rows_pre > 16) {
-        p.do_suffix = 0;
-        e = launch_attn(prefix_mma_kernel<D, true>, MmaCfg<D, true>::SMEM, p, 64, st);
-        p.do_suffix = 1;
+    if (pl.tc) {
+        if (p.n_pre > 0 && prefix_tc(p, D, st) != LKA_OK) return cudaErrorLaunchFailure;
         p.do_prefix = 0;
+    } else if (pl.rows_pre > 16) {
+        if constexpr (D == 256) {
+            TimedLaunch timer(st);
+            p.do_suffix = 0;
+            e = launch_attn<prefix_mma_kernel<D, true>>(MmaCfg<D, true>::SMEM, p, 64, st);
+            p.do_suffix = 1;
+            p.do_prefix = 0;
+            timer.stop();
+        }
     }
-    if (e == cudaSuccess) e = launch_attn(prefix_mma_kernel<D, false>, MmaCfg<D, false>::SMEM, p, 16, st);
-    timer.stop();
+    if (e == cudaSuccess) e = launch_attn<prefix_mma_kernel<D, false>>(MmaCfg<D, false>::SMEM, p, 16, st);
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
     constexpr int RPB = 128 / (D / 4);
@@ -569,7 +582,7 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
 template <int D>
 cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
     TimedLaunch timer(st);
-    const cudaError_t e = launch_attn(prefix_f32_kernel<D>, F32Cfg<D>::SMEM, p, 16, st);
+    const cudaError_t e = launch_attn<prefix_f32_kernel<D>>(F32Cfg<D>::SMEM, p, 16, st);
     timer.stop();
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;

@@ -1,6 +1,7 @@
 // prefix_attn.h -- parameters of the shared-prefix attention kernels.
 #pragma once
 
+#include "../../include/lka.h"
 #include "common.cuh"
 
 namespace lka {
@@ -22,6 +23,15 @@ struct PrefixParams {
     int page_size, max_pages, num_pages;
     float scale_log2;
 };
+
+// Row tiles of the tensor-core prefix kernel: the R rows of `seqs` sequences (R <= 128), or 128 of one sequence's R.
+struct PrefixTiles {
+    int seqs, per_seq;  // sequences per tile; tiles per sequence
+    int rows, n_tiles;  // rows of a tile, tiles per KV head
+    int box_rows;       // key rows per TMA box
+};
+PrefixTiles prefix_tiles(int B, int R);
+lka_status_t prefix_tc(const PrefixParams& p, int d, cudaStream_t st);
 
 // The prefix length, clamped into [0, Lp].
 __device__ __forceinline__ int prefix_length(const PrefixParams& p, bool report) {
