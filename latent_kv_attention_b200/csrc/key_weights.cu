@@ -15,29 +15,15 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "key_weights.h"
 #include "launch_util.h"
 #include "mma.cuh"
 
 namespace lka {
 
-struct KeyWeightParams {
-    const void* q;        // [B, h_q, s, D]
-    const void* k;        // [B, h_kv, Lmax, D] or pages [num_pages, h_kv, page_size, D]
-    const float* lse;     // [B, h_q, s] natural log
-    const int32_t* lens;  // [B]
-    const int32_t* table;
-    float* w;             // [B, h_kv, Lmax]
-    uint32_t* status;
-    int B, h_q, h_kv, s, Lmax, causal, accumulate, ratio;
-    int page_size, max_pages, num_pages;
-    int chunk;            // query rows staged at a time (a multiple of 8)
-    float scale_log2;
-};
-
 namespace {
 
 constexpr int kTile = 64;  // keys per block
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void write_weight(const KeyWeightParams& p, size_t at, float v) {
     p.w[at] = p.accumulate ? p.w[at] + v : v;
@@ -311,6 +297,7 @@ lka_status_t key_weights_run(const void* q, const void* k, const float* lse, con
     }
     const dim3 grid(cdiv(Lmax, kTile), h_kv, B);
     const cudaStream_t st = (cudaStream_t)stream;
+    if (dtype == LKA_BF16 && d <= 128 && s >= kKeyWeightsTcMinQueries) return key_weights_tc(p, d, st);
     cudaError_t e;
     if (dtype == LKA_FP32)
         e = d == 64 ? launch_f32<64>(p, grid, st) : launch_f32<128>(p, grid, st);

@@ -25,6 +25,8 @@ namespace lka {
 
 namespace {
 
+constexpr int kMaxSplits = 64, kMaxSlots = 2 * kMaxSplits;  // splits of the prefix and of a suffix at most, and both
+
 // ---- what a block works on ---------------------------------------------------------------------------------
 // Prefix: rows are the B * R query rows of a KV head (row i: sequence i / R, row i % R of its group).
 // Suffix: rows are the R rows of one sequence's group.  R = (h_q / h_kv) * s_q, row g is query g % s_q.
@@ -444,44 +446,70 @@ __global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
 }
 
 // ---- the merge ---------------------------------------------------------------------------------------------------
-// D / 4 threads per row.  A row's parts are the prefix splits its length reaches and the suffix splits with a key
-// that the row sees.
+// One warp per row.  A row's parts are the prefix splits its length reaches and the suffix splits with a key that the
+// row sees; the lanes fetch their lse together, then every lane joins its D / 32 values, eight parts in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p) {
-    constexpr int TPR = D / 4, RPB = 128 / TPR;
-    const size_t row = (size_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    const int c = threadIdx.x % TPR;
+    constexpr int VPL = D / 32;
+    __shared__ float fs[4][kMaxSlots];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const size_t row = (size_t)blockIdx.x * 4 + warp;
     if (row >= (size_t)p.B * p.h_q * p.s) return;
     const int b = (int)(row / ((size_t)p.h_q * p.s)), t = (int)(row % p.s);
     const int P = prefix_length(p, false);
     const int L = clamp_len(p.lens, b, p.Lmax, p.s, p.causal, p.status, false);
     const int seen = p.causal ? L - p.s + t + 1 : L;
-    const int np = cdiv(P, p.pre_tokens), ns = cdiv(seen, p.suf_tokens);
+    const int np = cdiv(P, p.pre_tokens), n = np + cdiv(seen, p.suf_tokens), gap = p.n_pre - np;
     const float* pl = p.part_lse + row * p.n_slots;
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.n_slots * D) + c;
-    float M = -INFINITY;
-    for (int i = 0; i < np; ++i) M = fmaxf(M, pl[i]);
-    for (int i = 0; i < ns; ++i) M = fmaxf(M, pl[p.n_pre + i]);
+    float x[kMaxSlots / 32], M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMaxSlots / 32; ++k) {
+        const int i = k * 32 + lane;
+        x[k] = i < n ? pl[i < np ? i : i + gap] : -INFINITY;
+        M = fmaxf(M, x[k]);
+    }
+#pragma unroll
+    for (int o = 16; o; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float sum = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < np + ns; ++i) {
-        const int slot = i < np ? i : p.n_pre + i - np;
-        const float f = M == -INFINITY ? 0.f : exp2f(pl[slot] - M);
-        const float4 x = po[(size_t)slot * TPR];
+#pragma unroll
+    for (int k = 0; k < kMaxSlots / 32; ++k) {
+        const float f = M == -INFINITY ? 0.f : exp2f(x[k] - M);
+        fs[warp][k * 32 + lane] = f;
         sum += f;
-        a = make_float4(fmaf(f, x.x, a.x), fmaf(f, x.y, a.y), fmaf(f, x.z, a.z), fmaf(f, x.w, a.w));
+    }
+#pragma unroll
+    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    const float* po = p.part_o + row * p.n_slots * D + lane * VPL;
+    float a[VPL] = {};
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float f = fs[warp][i];
+        const float* src = po + (size_t)(i < np ? i : i + gap) * D;
+        float y[VPL];
+        if constexpr (VPL == 2) {
+            *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VPL; e += 4) *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(src + e);
+        }
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) a[e] = fmaf(f, y[e], a[e]);
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    T* out = static_cast<T*>(p.out) + row * D + c * 4;
+    T* out = static_cast<T*>(p.out) + row * D + lane * VPL;
     if constexpr (sizeof(T) == 2) {
-        uint2 u;
-        u.x = bf16_pair(a.x * inv, a.y * inv);
-        u.y = bf16_pair(a.z * inv, a.w * inv);
-        *reinterpret_cast<uint2*>(out) = u;
+        uint32_t u[VPL / 2];
+#pragma unroll
+        for (int e = 0; e < VPL / 2; ++e) u[e] = bf16_pair(a[2 * e] * inv, a[2 * e + 1] * inv);
+        if constexpr (VPL == 2) *reinterpret_cast<uint32_t*>(out) = u[0];
+        if constexpr (VPL == 4) *reinterpret_cast<uint2*>(out) = make_uint2(u[0], u[1]);
+        if constexpr (VPL == 8) *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
-        *reinterpret_cast<float4*>(out) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+#pragma unroll
+        for (int e = 0; e < VPL; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
     }
-    if (p.lse && c == 0) p.lse[row] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // ---- planning ------------------------------------------------------------------------------------------------------
@@ -498,7 +526,7 @@ int split_keys(double units, double slots, int L, int tile) {
     const int lt = cdiv(std::max(L, 1), tile);
     int best = 1;
     double best_cost = -1.0;
-    for (int n = 1; n <= lt && n <= 64; ++n) {
+    for (int n = 1; n <= lt && n <= kMaxSplits; ++n) {
         const double w = units * n / slots;
         const double cost = fmax(ceil(w - 1e-9), w + 0.25) * (cdiv(lt, n) + 2);
         if (best_cost < 0.0 || cost < best_cost - 1e-9) {
@@ -524,14 +552,16 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     pl->rows_suf = 16;
     const int tile = f32 ? 32 : 64;
     const double slots = (double)sm_count() * (f32 ? 3 : d == 256 ? 1 : 2);
+    // the split knob, where it leaves at most kMaxSplits splits
     const int knob = split_tokens_knob();
+    auto by_knob = [knob](int L, int unit) { return cdiv(std::max(knob, cdiv(L, kMaxSplits)), unit) * unit; };
     if (pl->tc)
-        pl->pre_tokens = knob > 0 ? cdiv(knob, 128) * 128
+        pl->pre_tokens = knob > 0 ? by_knob(Lp, 128)
                                   : split_keys((double)h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), sm_count(), Lp, 128);
     else
-        pl->pre_tokens = knob > 0 ? cdiv(knob, tile) * tile
+        pl->pre_tokens = knob > 0 ? by_knob(Lp, tile)
                                   : split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile);
-    pl->suf_tokens = knob > 0 ? cdiv(knob, tile) * tile
+    pl->suf_tokens = knob > 0 ? by_knob(Lmax, tile)
                               : split_keys((double)h_kv * Bn * cdiv(R, pl->rows_suf), slots, Lmax, tile);
     pl->n_pre = cdiv(Lp, pl->pre_tokens);
     pl->n_suf = cdiv(Lmax, pl->suf_tokens);
@@ -574,8 +604,7 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_attn<prefix_mma_kernel<D, false>>(MmaCfg<D, false>::SMEM, p, 16, st);
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
-    constexpr int RPB = 128 / (D / 4);
-    prefix_merge_kernel<__nv_bfloat16, D><<<(unsigned)((rows + RPB - 1) / RPB), 128, 0, st>>>(p);
+    prefix_merge_kernel<__nv_bfloat16, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
     return cudaPeekAtLastError();
 }
 
@@ -586,8 +615,7 @@ cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
     timer.stop();
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
-    constexpr int RPB = 128 / (D / 4);
-    prefix_merge_kernel<float, D><<<(unsigned)((rows + RPB - 1) / RPB), 128, 0, st>>>(p);
+    prefix_merge_kernel<float, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
     return cudaPeekAtLastError();
 }
 
