@@ -5,8 +5,8 @@
 // lane) and streams tiles of 128 query rows of the group's heads (the columns) through a TMA
 // ring.  A key's weight is a sum along its own lane, so nothing crosses lanes and no P is
 // written back: per score one multiply-add with the row's normaliser, one exponential, one
-// addition.  Warp 8 loads, warp 9 issues the MMAs into four score buffers of tensor memory,
-// warps 0-3 and 4-7 take the score tiles in turn.  With few key tiles, the query tiles of one
+// addition.  Warp 16 loads, warp 17 issues the MMAs into four score buffers of tensor memory,
+// four groups of four warps take the score tiles in turn.  With few key tiles, the query tiles of one
 // key tile are dealt to the CTAs of a cluster, whose sums rank 0 adds in order.
 //
 // Bound: 16,384 exponentials per tile are 1024 cycles of the special-function unit (16 per
@@ -14,6 +14,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "host_util.h"
 #include "key_weights.h"
@@ -23,14 +24,15 @@
 namespace lka {
 
 namespace kwt {
-constexpr int TK = 128, TQ = 128, NT = 320, NBUF = 4;
+constexpr int TK = 128, TQ = 128, NBUF = 4;
+constexpr int NG = 4, NT = 32 * (4 * NG + 2);  // groups of four warps, one per score buffer
 template <int D>
 struct Cfg {
     static constexpr int NB = D / 64, BOX = 128 * 128, TILE = NB * BOX;
     static constexpr int NS = 4;  // query tiles in flight
     static constexpr int OFF_Q = TILE, OFF_LSE = OFF_Q + NS * TILE;
-    static constexpr int OFF_SUM = OFF_LSE + 4 * TQ * 4;  // [2 groups][2 parities][TQ]
-    static constexpr int OFF_BAR = OFF_SUM + 2 * TK * 4;  // [2 groups][TK]
+    static constexpr int OFF_SUM = OFF_LSE + 2 * NG * TQ * 4;  // [NG][2 parities][TQ]
+    static constexpr int OFF_BAR = OFF_SUM + NG * TK * 4;      // [NG][TK]
     static constexpr int SMEM = 1024 + OFF_BAR + 256;
 };
 }  // namespace kwt
@@ -69,9 +71,10 @@ __global__ void __launch_bounds__(kwt::NT, 1)
     __shared__ int s_abort;
 
     const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
-    const int j0 = (int)blockIdx.x / cluster * TK, kvh = blockIdx.y, b = blockIdx.z;
+    // key tiles are the slowest grid dimension: the causal half makes the first ones the longest, and they start first
+    const int j0 = (int)blockIdx.z * TK, kvh = (int)blockIdx.x / cluster, b = blockIdx.y;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int L = clamp_len(p.lens, b, p.Lmax, p.s, p.causal, p.status, threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0);
+    const int L = clamp_len(p.lens, b, p.Lmax, p.s, p.causal, p.status, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0);
     const size_t wrow = ((size_t)b * p.h_kv + kvh) * p.Lmax;
     if (j0 >= L) {  // the whole cluster: one key tile
         const int j = j0 + threadIdx.x;
@@ -96,7 +99,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
         }
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 4 * NG + 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -104,9 +107,8 @@ __global__ void __launch_bounds__(kwt::NT, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    float sum = 0.f;
 
-    if (warp == 8) {
+    if (warp == 4 * NG) {
         if (lane == 0) {
             const uint32_t kb = smem_u32(k_full);
             mbar_arrive_expect_tx(kb, C::TILE);
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
                 mbar_wait(smem_u32(&full[i % C::NS]), (i / C::NS) & 1, p.status);
             mbar_wait(kb, 0, p.status);
         }
-    } else if (warp == 9) {
+    } else if (warp == 4 * NG + 1) {
         constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
         bool ok = mbar_wait(smem_u32(k_full), 0, p.status);
         for (int i = 0; ok && i < n_mine; ++i) {
@@ -186,67 +188,78 @@ __global__ void __launch_bounds__(kwt::NT, 1)
         };
         float next = lse_of(grp);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        bool ok = true;
-        for (int i = grp, turn = 0; i < n_mine; i += 2, ++turn) {
-            float* lb = ls + (turn & 1) * TQ;
-            lb[r] = next;
-            named_barrier(1 + grp, 128);
-            next = lse_of(i + 2);
-            const int buf = i % NBUF;
-            if (ok) ok = mbar_wait(smem_u32(&s_ready[buf]), (i / NBUF) & 1, p.status);
-            tc_fence_after();
-            const int n = (int)rank + i * cluster, t0 = start + n % per * TQ;
-            // query t sees key j when j <= L - s + t: tiles whose first query sees the last key need no mask
-            const bool masked = p.causal && j0 + TK - 1 > L - p.s + t0;
-            const int first = masked ? key - (L - p.s) - t0 : -1;  // rows from `first` on see the key
-            const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+        // one score tile, 32 columns at a time; MASK: rows before `first` do not see the key
+        auto tile = [&](auto mask, uint32_t ts, const float* lb, int first, uint32_t release) {
+            constexpr bool MASK = decltype(mask)::value;
+            uint32_t sr[2][32];
+            tmem_ld16(ts, sr[0]);
+            tmem_ld16(ts + 16, sr[0] + 16);
 #pragma unroll
-            for (int c0 = 0; c0 < TQ; c0 += 64) {
-                uint32_t sr[64];
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) tmem_ld16(tmem + lanes + buf * 128 + c0 + c, sr + c);
+            for (int q = 0; q < TQ / 32; ++q) {
                 tmem_ld_wait();
-                if (c0 == 64) {  // the last read of the buffer
+                if (q + 1 < TQ / 32) {
+                    tmem_ld16(ts + 32 * (q + 1), sr[(q + 1) & 1]);
+                    tmem_ld16(ts + 32 * (q + 1) + 16, sr[(q + 1) & 1] + 16);
+                } else {  // the last read of the buffer
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_free[buf]));
+                    if (lane == 0) mbar_arrive(release);
                 }
+                const uint32_t* x = sr[q & 1];
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(lb + c0 + c);
-                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc,
-                                                 make_float2(-l4.x, -l4.y));
-                    const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sc,
-                                                 make_float2(-l4.z, -l4.w));
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(lb + 32 * q + c);
+                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc,
+                                                 make_float2(l4.x, l4.y));
+                    const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc,
+                                                 make_float2(l4.z, l4.w));
                     float2 e0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
                     float2 e1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
-                    if (masked) {
-                        if (c0 + c < first) e0.x = 0.f;
-                        if (c0 + c + 1 < first) e0.y = 0.f;
-                        if (c0 + c + 2 < first) e1.x = 0.f;
-                        if (c0 + c + 3 < first) e1.y = 0.f;
+                    if constexpr (MASK) {
+                        if (32 * q + c < first) e0.x = 0.f;
+                        if (32 * q + c + 1 < first) e0.y = 0.f;
+                        if (32 * q + c + 2 < first) e1.x = 0.f;
+                        if (32 * q + c + 3 < first) e1.y = 0.f;
                     }
                     acc[0] = __fadd2_rn(acc[0], e0);
                     acc[1] = __fadd2_rn(acc[1], e1);
                 }
             }
+        };
+        bool ok = true;
+        for (int i = grp, turn = 0; i < n_mine; i += NG, ++turn) {
+            float* lb = ls + (turn & 1) * TQ;
+            lb[r] = -next;
+            named_barrier(1 + grp, 128);
+            next = lse_of(i + NG);
+            const int buf = i % NBUF;
+            if (ok) ok = mbar_wait(smem_u32(&s_ready[buf]), (i / NBUF) & 1, p.status);
+            tc_fence_after();
+            const int n = (int)rank + i * cluster, t0 = start + n % per * TQ;
+            const uint32_t ts = tmem + lanes + buf * 128, release = smem_u32(&s_free[buf]);
+            // query t sees key j when j <= L - s + t: a tile whose first query sees the last key needs no mask
+            if (p.causal && j0 + TK - 1 > L - p.s + t0)
+                tile(std::true_type{}, ts, lb, key - (L - p.s) - t0, release);
+            else
+                tile(std::false_type{}, ts, lb, 0, release);
         }
         if (!ok) s_abort = 1;
-        sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-        reinterpret_cast<float*>(smem + C::OFF_SUM)[grp * TK + r] = sum;
+        reinterpret_cast<float*>(smem + C::OFF_SUM)[grp * TK + r] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 4 * NG + 1) tmem_dealloc(tmem, 512);
     if (cluster > 1) cluster_sync();
     if (rank == 0 && threadIdx.x < TK) {
         const int key = j0 + threadIdx.x;
         const uint32_t at = smem_u32(smem + C::OFF_SUM) + threadIdx.x * 4;
         float w = 0.f;
         for (int c = 0; c < cluster; ++c)
-            w += cluster > 1 ? cluster_load(at, c) + cluster_load(at + TK * 4, c)
-                             : reinterpret_cast<float*>(smem + C::OFF_SUM)[threadIdx.x] +
-                                   reinterpret_cast<float*>(smem + C::OFF_SUM)[TK + threadIdx.x];
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                w += cluster > 1 ? cluster_load(at + g * TK * 4, c)
+                                 : reinterpret_cast<const float*>(smem + C::OFF_SUM)[g * TK + threadIdx.x];
         if (key < L)
             p.w[wrow + key] = p.accumulate ? p.w[wrow + key] + w : w;
         else if (key < p.Lmax && !p.accumulate)
@@ -271,6 +284,7 @@ static lka_status_t key_weights_tc_run(const KeyWeightParams& p, cudaStream_t st
     if (!make_tmap_nd(&tq, BF, p.q, 3, qd, qs, qb) || !make_tmap_nd(&tk, BF, p.k, 3, kd, ks, kb)) return LKA_ERR_CUDA;
     if (allow_smem<key_weights_tc_kernel<D>>(C::SMEM) != cudaSuccess) return LKA_ERR_CUDA;
     const int key_tiles = cdiv(p.Lmax, kwt::TK);
+    if (key_tiles > 65535) return LKA_ERR_UNSUPPORTED;
     // clusters share a key tile's queries while the key tiles alone leave SMs idle, and while every CTA keeps at
     // least two query tiles
     const long long units = (long long)key_tiles * p.h_kv * p.B;
@@ -278,7 +292,7 @@ static lka_status_t key_weights_tc_run(const KeyWeightParams& p, cudaStream_t st
     int cluster = 1;
     while (cluster < 8 && units * cluster * 2 <= 4LL * sm_count() && q_tiles >= 4 * cluster) cluster *= 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(key_tiles * cluster, p.h_kv, p.B);
+    cfg.gridDim = dim3(p.h_kv * cluster, p.B, key_tiles);
     cfg.blockDim = dim3(kwt::NT);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;

@@ -522,13 +522,14 @@ struct PrefixPlan {
 
 // Keys per split of `units` row blocks over L keys: the split count n <= 64 that minimises waves x (tiles per split
 // + 2), the 2 for a block's start and end, where the waves of w = units n / slots cost max(ceil(w), w + 1/4).
-int split_keys(double units, double slots, int L, int tile) {
+// `ragged` lengths leave an average tail beyond the mean; equal ones end together and cost ceil(w) waves.
+int split_keys(double units, double slots, int L, int tile, bool ragged = true) {
     const int lt = cdiv(std::max(L, 1), tile);
     int best = 1;
     double best_cost = -1.0;
     for (int n = 1; n <= lt && n <= kMaxSplits; ++n) {
         const double w = units * n / slots;
-        const double cost = fmax(ceil(w - 1e-9), w + 0.25) * (cdiv(lt, n) + 2);
+        const double cost = fmax(ceil(w - 1e-9), ragged ? w + 0.25 : w) * (cdiv(lt, n) + 2);
         if (best_cost < 0.0 || cost < best_cost - 1e-9) {
             best_cost = cost;
             best = n;
@@ -557,7 +558,7 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     auto by_knob = [knob](int L, int unit) { return cdiv(std::max(knob, cdiv(L, kMaxSplits)), unit) * unit; };
     if (pl->tc)
         pl->pre_tokens = knob > 0 ? by_knob(Lp, 128)
-                                  : split_keys((double)h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), sm_count(), Lp, 128);
+                                  : split_keys((double)h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), sm_count(), Lp, 128, false);
     else
         pl->pre_tokens = knob > 0 ? by_knob(Lp, tile)
                                   : split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile);

@@ -10,7 +10,7 @@
 // the tensor pipe works for the other.  P_i overwrites S_i in tensor memory: the MMAs run in
 // the order they are issued, so S_i(j + 1) follows the P V product that reads P_i(j), and
 // s_ready(j + 1) also tells that O_i holds tile j, which makes rescaling O_i safe then.  P is
-// handed over in two halves of 64 keys, so that P V starts on the first while the second is
+// handed over in quarters of 32 keys, so that P V starts on the first while the next is
 // still in its exponentials.
 //
 // Bound: 2 x 128 x 128 x 4 d FLOPs per key tile pair at d = 128 are 2080 tensor cycles; its
@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     uint64_t* full = bars + 1;
     uint64_t* empty = full + C::NS;
     uint64_t* s_ready = empty + C::NS;  // [2]
-    uint64_t* p_ready = s_ready + 2;    // [2][2]: row tile, half of the keys
-    uint64_t* o_done = p_ready + 4;     // [2]
+    uint64_t* p_ready = s_ready + 2;    // [2][4]: row tile, quarter of the keys
+    uint64_t* o_done = p_ready + 8;     // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
     __shared__ int s_abort;
 
@@ -80,8 +80,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_ready[i]), 1);
-            mbar_init(smem_u32(&p_ready[2 * i]), 4);
-            mbar_init(smem_u32(&p_ready[2 * i + 1]), 4);
+            for (int h = 0; h < 4; ++h) mbar_init(smem_u32(&p_ready[4 * i + h]), 4);
             mbar_init(smem_u32(&o_done[i]), 1);
         }
         fence_barrier_init();
@@ -183,8 +182,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
             }
             for (int i = 0; ok && i < n_qt; ++i) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!mbar_wait(smem_u32(&p_ready[2 * i + h]), j & 1, p.status)) {
+                for (int h = 0; h < 4; ++h) {
+                    if (!mbar_wait(smem_u32(&p_ready[4 * i + h]), j & 1, p.status)) {
                         ok = false;
                         break;
                     }
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                     if (lane == 0) {
                         const uint32_t va = smem_u32(stage(2 * j + 1));
 #pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        for (int k = 2 * h; k < 2 * h + 2; ++k)
                             umma_ts(tmem + C::T_O + i * D, tmem + C::T_S + i * 128 + k * 8,
                                     smem_desc_sw128(va + k * 2048, C::BOX, 1024), id_pv, (j | k) != 0);
                     }
@@ -238,63 +237,69 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                 for (int c = 0; c < TK; ++c) f[c] = c < valid ? f[c] * mul : -INFINITY;
                 mul = 1.f;
             }
+            const float2 mul2 = make_float2(mul, mul);
+            // a quarter of the row: 32 probabilities against the reference maximum `ref`, as bf16 pairs, and their sum
+            uint32_t pk[16];
+            float2 part;
+            auto quarter = [&](int c0, float ref) {
+                const float2 neg2 = make_float2(-ref, -ref);
+                float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 x = __ffma2_rn(make_float2(f[c0 + c], f[c0 + c + 1]), mul2, neg2);
+                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    s2[(c / 2) & 1] = __fadd2_rn(s2[(c / 2) & 1], e);
+                    pk[c / 2] = pack_bf16x2(e.x, e.y);
+                }
+                part = __fadd2_rn(s2[0], s2[1]);
+            };
+            // The reference moves only when a score exceeds it by 2^8, which is rare after the first tile: the first
+            // quarter is computed against the old one while the maximum is still being found.
+            quarter(0, m == -INFINITY ? 0.f : m);
             float mx;
             if (mul >= 0.f) {
-                float a[8];
+                float a[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) a[c] = f[c];
+                for (int c = 0; c < 4; ++c) a[c] = f[c];
 #pragma unroll
-                for (int c = 8; c < TK; ++c) a[c % 8] = fmaxf(a[c % 8], f[c]);
-                mx = tree_max<8>(a) * mul;
+                for (int c = 4; c < TK; ++c) a[c % 4] = fmaxf(a[c % 4], f[c]);
+                mx = tree_max<4>(a) * mul;
             } else {
                 float a = f[0];
 #pragma unroll
                 for (int c = 1; c < TK; ++c) a = fminf(a, f[c]);
                 mx = a * mul;
             }
-            // the reference maximum moves only when a score exceeds it by 2^8
-            if (m == -INFINITY) {
-                m = mx;
-            } else {
-                const bool grow = mx > m + 8.f;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float alpha = grow ? fast_exp2(m - mx) : 1.f;
-                    if (grow) m = mx;
-                    l2.x *= alpha;
-                    l2.y *= alpha;
-                    if (j > 0) {
+            const bool grow = m == -INFINITY || mx > m + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float to_m = grow ? mx : m;
+                const float alpha = m == -INFINITY || to_m == m ? 1.f : fast_exp2(m - to_m);
+                m = to_m;
+                l2.x *= alpha;
+                l2.y *= alpha;
+                if (j > 0) {  // s_ready also says that O holds the tiles before this one
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(to + c, o);
-                            tmem_ld_wait();
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + c, o);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(to + c, o);
-                        }
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st16(to + c, o);
                     }
                 }
+                quarter(0, m == -INFINITY ? 0.f : m);
             }
             const float ms = m == -INFINITY ? 0.f : m;
-            const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-ms, -ms);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float2 x = __ffma2_rn(make_float2(f[c0 + c], f[c0 + c + 1]), mul2, neg2);
-                        const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        l2 = __fadd2_rn(l2, e);
-                        pk[c / 2] = pack_bf16x2(e.x, e.y);
-                    }
-                    tmem_st16(ts + c0 / 2, pk);
-                }
+            for (int h = 0; h < 4; ++h) {
+                if (h) quarter(32 * h, ms);
+                l2 = __fadd2_rn(l2, part);
+                tmem_st16(ts + 16 * h, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * i + h]));
+                if (lane == 0) mbar_arrive(smem_u32(&p_ready[4 * i + h]));
             }
         }
         if (ok) ok = mbar_wait(smem_u32(&o_done[i]), 0, p.status);
