@@ -3,19 +3,20 @@
 // all sequences that use one KV head.
 //
 // One CTA takes two tiles of up to 128 query rows of one KV head and a range of the
-// prefix's keys, in tiles of 128 keys; the two row tiles share every K and V tile.  Warp 8
-// streams K and V with TMA through one ring; warp 9 issues the MMAs, per key tile j and row
-// tile i: O_i += P_i(j) V_j, then S_i(j + 1) = Q_i K_{j+1}^T; warps 0-3 and 4-7 are the
-// softmax of row tile 0 and 1, one thread per row.  While one row tile is in its softmax,
-// the tensor pipe works for the other.  P_i overwrites S_i in tensor memory: the MMAs run in
-// the order they are issued, so S_i(j + 1) follows the P V product that reads P_i(j), and
-// s_ready(j + 1) also tells that O_i holds tile j, which makes rescaling O_i safe then.  P is
-// handed over in quarters of 32 keys, so that P V starts on the first while the next is
-// still in its exponentials.
+// prefix's keys; the two row tiles share every K and V tile of 128 keys, which warp 8 streams
+// with TMA through one ring.  Scores are made 64 keys at a time into two buffers per row tile:
+// one thread of warp 9 + i issues the MMAs of row tile i, per block n: O_i += P_i(n) V_n, then
+// S_i(n + 2) = Q_i K_{n+2}^T; warps 0-3 and 4-7 are the softmax of row tile 0 and 1, one
+// thread per row, which finds S_i(n + 1) made while it works on block n.  P_i(n) overwrites
+// S_i(n) in tensor memory: MMAs of one thread run in the order they are issued, so S_i(n + 2)
+// follows the P V product that reads P_i(n).
 //
-// Bound: 2 x 128 x 128 x 4 d FLOPs per key tile pair at d = 128 are 2080 tensor cycles; its
-// 32,768 exponentials are 2048 cycles of the special-function unit (16 per cycle and SM), so
-// both pipes are full together.  Below about 256 rows per KV head the prefix's bytes bound.
+// Bound: per 128 keys the 2 x 128 x 128 x 4 d FLOPs take 2576 tensor cycles at d = 128 (2080
+// at the full rate; an N = 64 MMA costs 48 cycles, not 32) and 32,768 exponentials 2048 cycles
+// of the special-function unit (16 per cycle and SM).  One score buffer of 128 keys per row
+// tile ran at 5000 cycles: the chain score product, softmax, value product of each row tile was
+// then serial, and the two row tiles fell into step.  Below about 256 rows per KV head the
+// prefix's bytes bound.
 #include <math.h>
 
 #include <algorithm>
@@ -28,7 +29,8 @@
 namespace lka {
 
 namespace ptc {
-constexpr int TK = 128, NT = 320;
+constexpr int TK = 128, TB = 64;  // keys per K / V tile, per block of scores
+constexpr int W_LOAD = 8, W_MMA = 9, NT = 352;  // warps 0-3 and 4-7: softmax; 8: loads; 9 and 10: MMAs
 template <int D>
 struct Cfg {
     static constexpr int NB = D / 64;            // 64-column boxes of a row
@@ -56,11 +58,13 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     uint64_t* q_full = bars;
     uint64_t* full = bars + 1;
     uint64_t* empty = full + C::NS;
-    uint64_t* s_ready = empty + C::NS;  // [2]
-    uint64_t* p_ready = s_ready + 2;    // [2][4]: row tile, quarter of the keys
-    uint64_t* o_done = p_ready + 8;     // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
-    __shared__ int s_abort;
+    uint64_t* s_ready = empty + C::NS;  // [2][2]: row tile, score buffer
+    uint64_t* p_ready = s_ready + 4;    // [2][2]
+    uint64_t* o_ready = p_ready + 4;    // [2]
+    uint64_t* o_done = o_ready + 2;     // [2]
+    uint64_t* v_tail = o_done + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_tail + 1);
+    __shared__ int s_abort, s_loaded;
 
     const int pairs = cdiv(g.n_tiles, 2);
     const int pair = blockIdx.x % pairs, split = (blockIdx.x / pairs) % p.n_pre, kvh = blockIdx.x / (pairs * p.n_pre);
@@ -69,23 +73,28 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     const int P = prefix_length(p, threadIdx.x == 0 && blockIdx.x == 0);
     const int kbeg = split * p.pre_tokens, kend = min(P, kbeg + p.pre_tokens);
     if (kend <= kbeg) return;
-    const int n_kt = cdiv(kend - kbeg, TK);
+    const int n_kt = cdiv(kend - kbeg, TK), nb = cdiv(kend - kbeg, TB);  // tiles of keys, blocks of scores
 
     if (threadIdx.x == 0) {
         s_abort = 0;
+        s_loaded = 0;
         mbar_init(smem_u32(q_full), 1);
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&empty[s]), n_qt);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&s_ready[i]), 1);
-            for (int h = 0; h < 4; ++h) mbar_init(smem_u32(&p_ready[4 * i + h]), 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_u32(&s_ready[2 * i + h]), 1);
+                mbar_init(smem_u32(&p_ready[2 * i + h]), 4);
+            }
+            mbar_init(smem_u32(&o_ready[i]), 1);
             mbar_init(smem_u32(&o_done[i]), 1);
         }
+        mbar_init(smem_u32(v_tail), 1);
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == W_LOAD) {
         tmem_alloc(tmem_slot, C::T_COLS);
         tmem_relinquish();
     }
@@ -94,7 +103,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 8) {
+    if (warp == W_LOAD) {
         // ------------------------------ producer: Q, then K_0, V_0, K_1, V_1, ... ------------------------------
         if (lane == 0) {
             const uint32_t qb = smem_u32(q_full);
@@ -141,135 +150,121 @@ __global__ void __launch_bounds__(ptc::NT, 1)
             for (int n = issued - 1; n >= 0 && n >= issued - C::NS; --n)
                 mbar_wait(smem_u32(&full[n % C::NS]), (n / C::NS) & 1, p.status);
             mbar_wait(qb, 0, p.status);
+            *(volatile int*)&s_loaded = issued;
         }
-    } else if (warp == 9) {
-        // ------------------------------ MMA issuer ------------------------------
-        constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
-        constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
-        bool ok = mbar_wait(smem_u32(q_full), 0, p.status);
-        auto stage = [&](int n) { return smem + C::OFF_RING + (n % C::NS) * C::TILE; };
-        auto wait_full = [&](int n) { return mbar_wait(smem_u32(&full[n % C::NS]), (n / C::NS) & 1, p.status); };
-        auto scores = [&](int i, int j) {  // S_i(j)
-            if (lane == 0) {
-                const uint32_t qa = smem_u32(smem + i * C::TILE), ka = smem_u32(stage(2 * j));
+        __syncwarp();
+        const int n = 2 * n_kt - 1, valid = kend - (kbeg + n / 2 * TK);
+        if (valid < TK && *(volatile int*)&s_loaded == 2 * n_kt) {
+            // the last tile's value rows past the keys may hold anything, and 0 x NaN would reach every row: zeros
+            mbar_wait(smem_u32(&full[n % C::NS]), (n / C::NS) & 1, p.status);
+            uint8_t* v = smem + C::OFF_RING + n % C::NS * C::TILE;
+            const int rows = TK - valid;
+            for (int x = lane; x < C::NB * rows * 8; x += 32)
+                *reinterpret_cast<uint4*>(v + x / (rows * 8) * C::BOX + (valid + x / 8 % rows) * 128 + x % 8 * 16) =
+                    make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(v_tail));
+        }
+    } else if (warp == W_MMA || warp == W_MMA + 1) {
+        // ------------------------------ MMA issuers: one thread per row tile ------------------------------
+        const int i = warp - W_MMA;
+        if (i < n_qt && lane == 0) {
+            constexpr uint32_t id_qk = idesc_bf16_f32(128, TB, false, false);
+            constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
+            constexpr int B4 = C::BOX >> 4;
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + i * C::TILE), 16, 1024);
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::OFF_RING), C::BOX, 1024);
+            const uint32_t ts = tmem + C::T_S + i * 2 * TB, to = tmem + C::T_O + i * D;
+            int ks = 0, vs = 1, kp = 0, vp = 0;  // ring stages of the current K and V tile, and their phases
+            auto step = [&](int& st, int& ph) {
+                st += 2;
+                if (st >= C::NS) {
+                    st -= C::NS;
+                    ph ^= 1;
+                }
+            };
+            auto scores = [&](int n) {  // S(n)
+                const uint64_t kd = k_desc + (uint64_t)(ks * (C::TILE >> 4) + (n & 1) * (TB * 128 >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_ss(tmem + C::T_S + i * 128, smem_desc_sw128(qa + (k / 4) * C::BOX + (k % 4) * 32, 16, 1024),
-                            smem_desc_sw128(ka + (k / 4) * C::BOX + (k % 4) * 32, 16, 1024), id_qk, k != 0);
-                umma_commit(smem_u32(&s_ready[i]));
-                if (i == n_qt - 1) umma_commit(smem_u32(&empty[(2 * j) % C::NS]));
-            }
-            __syncwarp();
-        };
-        if (ok) ok = wait_full(0);
-        if (ok) {
-            tc_fence_after();
-            for (int i = 0; i < n_qt; ++i) scores(i, 0);
-        }
-        for (int j = 0; ok && j < n_kt; ++j) {
-            ok = wait_full(2 * j + 1);
-            if (!ok) break;
-            const int valid = kend - (kbeg + j * TK);
-            if (valid < TK) {
-                // value rows past the keys may hold anything; 0 x NaN would reach every row
-                uint8_t* v = stage(2 * j + 1);
-                const int rows = TK - valid;
-                for (int x = lane; x < C::NB * rows * 8; x += 32)
-                    *reinterpret_cast<uint4*>(v + x / (rows * 8) * C::BOX + (valid + x / 8 % rows) * 128 + x % 8 * 16) =
-                        make_uint4(0, 0, 0, 0);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-            }
-            for (int i = 0; ok && i < n_qt; ++i) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (!mbar_wait(smem_u32(&p_ready[4 * i + h]), j & 1, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t va = smem_u32(stage(2 * j + 1));
-#pragma unroll
-                        for (int k = 2 * h; k < 2 * h + 2; ++k)
-                            umma_ts(tmem + C::T_O + i * D, tmem + C::T_S + i * 128 + k * 8,
-                                    smem_desc_sw128(va + k * 2048, C::BOX, 1024), id_pv, (j | k) != 0);
-                    }
-                    __syncwarp();
+                    umma_ss(ts + (n & 1) * TB, q_desc + (k / 4) * B4 + (k % 4) * 2, kd + (k / 4) * B4 + (k % 4) * 2, id_qk,
+                            k != 0);
+                umma_commit(smem_u32(&s_ready[2 * i + (n & 1)]));
+                if ((n & 1) || n == nb - 1) {
+                    umma_commit(smem_u32(&empty[ks]));
+                    step(ks, kp);
                 }
+            };
+            bool ok = mbar_wait(smem_u32(q_full), 0, p.status) && mbar_wait(smem_u32(&full[0]), 0, p.status);
+            if (ok) {
+                tc_fence_after();
+                scores(0);
+                if (nb > 1) scores(1);
+            }
+            for (int n = 0; ok && n < nb; ++n) {
+                if (!(n & 1)) {
+                    ok = mbar_wait(smem_u32(&full[vs]), vp, p.status);
+                    if (ok && kend - (kbeg + n * TB) < TK) ok = mbar_wait(smem_u32(v_tail), 0, p.status);
+                    if (ok && n + 2 < nb) ok = mbar_wait(smem_u32(&full[ks]), kp, p.status);
+                }
+                if (ok) ok = mbar_wait(smem_u32(&p_ready[2 * i + (n & 1)]), (n >> 1) & 1, p.status);
                 if (!ok) break;
-                if (lane == 0) {
-                    if (i == n_qt - 1) umma_commit(smem_u32(&empty[(2 * j + 1) % C::NS]));
-                    if (j == n_kt - 1) umma_commit(smem_u32(&o_done[i]));
-                }
-                __syncwarp();
-                if (j + 1 < n_kt) {
-                    if (i == 0 && !wait_full(2 * (j + 1))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    scores(i, j + 1);
+                tc_fence_after();
+                const uint64_t vd = v_desc + (uint64_t)(vs * (C::TILE >> 4) + (n & 1) * (TB * 128 >> 4));
+#pragma unroll
+                for (int k = 0; k < TB / 16; ++k)
+                    umma_ts(to, ts + (n & 1) * TB + k * 8, vd + k * (2048 >> 4), id_pv, (n | k) != 0);
+                umma_commit(smem_u32(&o_ready[i]));
+                if (n == nb - 1) umma_commit(smem_u32(&o_done[i]));
+                if (n + 2 < nb) scores(n + 2);
+                if ((n & 1) || n == nb - 1) {
+                    umma_commit(smem_u32(&empty[vs]));
+                    step(vs, vp);
                 }
             }
+            if (!ok) s_abort = 1;
         }
-        if (!ok) s_abort = 1;
     } else if (warp / 4 < n_qt) {
         // ------------------------------ softmax: one thread per query row ------------------------------
         const int i = warp / 4, r = (warp % 4) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
-        const uint32_t ts = tmem + lanes + C::T_S + i * 128, to = tmem + lanes + C::T_O + i * D;
+        const uint32_t to = tmem + lanes + C::T_O + i * D;
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
-        for (int j = 0; j < n_kt; ++j) {
-            if (ok) ok = mbar_wait(smem_u32(&s_ready[i]), j & 1, p.status);
+        for (int n = 0; n < nb; ++n) {
+            const uint32_t ts = tmem + lanes + C::T_S + (2 * i + (n & 1)) * TB;
+            if (ok) ok = mbar_wait(smem_u32(&s_ready[2 * i + (n & 1)]), (n >> 1) & 1, p.status);
             tc_fence_after();
-            uint32_t sr[TK];
+            uint32_t sr[TB];
 #pragma unroll
-            for (int c = 0; c < TK; c += 16) tmem_ld16(ts + c, sr + c);
+            for (int c = 0; c < TB; c += 16) tmem_ld16(ts + c, sr + c);
             tmem_ld_wait();
             float* f = reinterpret_cast<float*>(sr);
             float mul = p.scale_log2;
-            const int valid = kend - (kbeg + j * TK);
-            if (valid < TK) {
+            const int valid = kend - (kbeg + n * TB);
+            if (valid < TB) {
 #pragma unroll
-                for (int c = 0; c < TK; ++c) f[c] = c < valid ? f[c] * mul : -INFINITY;
+                for (int c = 0; c < TB; ++c) f[c] = c < valid ? f[c] * mul : -INFINITY;
                 mul = 1.f;
             }
-            const float2 mul2 = make_float2(mul, mul);
-            // a quarter of the row: 32 probabilities against the reference maximum `ref`, as bf16 pairs, and their sum
-            uint32_t pk[16];
-            float2 part;
-            auto quarter = [&](int c0, float ref) {
-                const float2 neg2 = make_float2(-ref, -ref);
-                float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const float2 x = __ffma2_rn(make_float2(f[c0 + c], f[c0 + c + 1]), mul2, neg2);
-                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                    s2[(c / 2) & 1] = __fadd2_rn(s2[(c / 2) & 1], e);
-                    pk[c / 2] = pack_bf16x2(e.x, e.y);
-                }
-                part = __fadd2_rn(s2[0], s2[1]);
-            };
-            // The reference moves only when a score exceeds it by 2^8, which is rare after the first tile: the first
-            // quarter is computed against the old one while the maximum is still being found.
-            quarter(0, m == -INFINITY ? 0.f : m);
             float mx;
             if (mul >= 0.f) {
                 float a[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) a[c] = f[c];
 #pragma unroll
-                for (int c = 4; c < TK; ++c) a[c % 4] = fmaxf(a[c % 4], f[c]);
+                for (int c = 4; c < TB; ++c) a[c % 4] = fmaxf(a[c % 4], f[c]);
                 mx = tree_max<4>(a) * mul;
             } else {
                 float a = f[0];
 #pragma unroll
-                for (int c = 1; c < TK; ++c) a = fminf(a, f[c]);
+                for (int c = 1; c < TB; ++c) a = fminf(a, f[c]);
                 mx = a * mul;
             }
+            // the reference maximum moves only when a score exceeds it by 2^8: rarely after the first block
             const bool grow = m == -INFINITY || mx > m + 8.f;
             if (__any_sync(0xffffffffu, grow)) {
                 const float to_m = grow ? mx : m;
@@ -277,7 +272,10 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                 m = to_m;
                 l2.x *= alpha;
                 l2.y *= alpha;
-                if (j > 0) {  // s_ready also says that O holds the tiles before this one
+                if (n > 0) {
+                    // O has to hold block n - 1; s_ready(n) told that it holds n - 2, and n waits for this warp
+                    if (ok) ok = mbar_wait(smem_u32(&o_ready[i]), (n - 1) & 1, p.status);
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
@@ -288,19 +286,27 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                         tmem_st16(to + c, o);
                     }
                 }
-                quarter(0, m == -INFINITY ? 0.f : m);
             }
             const float ms = m == -INFINITY ? 0.f : m;
+            const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-ms, -ms);
+            float2 part[2] = {l2, make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                if (h) quarter(32 * h, ms);
-                l2 = __fadd2_rn(l2, part);
+            for (int h = 0; h < TB / 32; ++h) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 x = __ffma2_rn(make_float2(f[32 * h + c], f[32 * h + c + 1]), mul2, neg2);
+                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    part[(c / 2) & 1] = __fadd2_rn(part[(c / 2) & 1], e);
+                    pk[c / 2] = pack_bf16x2(e.x, e.y);
+                }
                 tmem_st16(ts + 16 * h, pk);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_ready[4 * i + h]));
             }
+            l2 = __fadd2_rn(part[0], part[1]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * i + (n & 1)]));
         }
         if (ok) ok = mbar_wait(smem_u32(&o_done[i]), 0, p.status);
         if (!ok) s_abort = 1;
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, C::T_COLS);
+    if (warp == W_LOAD) tmem_dealloc(tmem, C::T_COLS);
 }
 
 PrefixTiles prefix_tiles(int B, int R) {
