@@ -30,7 +30,7 @@ namespace lka {
 
 namespace ptc {
 constexpr int TK = 128, TB = 64;  // keys per K / V tile, per block of scores
-constexpr int W_LOAD = 8, W_MMA = 9, NT = 352;  // warps 0-3 and 4-7: softmax; 8: loads; 9 and 10: MMAs
+constexpr int W_LOAD = 8, W_MMA = 9, NT = 416;  // warps 0-3 and 4-7: softmax; 8: loads; 9 + 2i, 10 + 2i: scores, values
 template <int D>
 struct Cfg {
     static constexpr int NB = D / 64;            // 64-column boxes of a row
@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     uint64_t* empty = full + C::NS;
     uint64_t* s_ready = empty + C::NS;  // [2][2]: row tile, score buffer
     uint64_t* p_ready = s_ready + 4;    // [2][2]
-    uint64_t* o_ready = p_ready + 4;    // [2]
-    uint64_t* o_done = o_ready + 2;     // [2]
+    uint64_t* o_ready = p_ready + 4;    // [2][2]: the block of that buffer is in O
+    uint64_t* o_done = o_ready + 4;     // [2]
     uint64_t* v_tail = o_done + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_tail + 1);
     __shared__ int s_abort, s_loaded;
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
             for (int h = 0; h < 2; ++h) {
                 mbar_init(smem_u32(&s_ready[2 * i + h]), 1);
                 mbar_init(smem_u32(&p_ready[2 * i + h]), 4);
+                mbar_init(smem_u32(&o_ready[2 * i + h]), 1);
             }
-            mbar_init(smem_u32(&o_ready[i]), 1);
             mbar_init(smem_u32(&o_done[i]), 1);
         }
         mbar_init(smem_u32(v_tail), 1);
@@ -166,62 +166,63 @@ __global__ void __launch_bounds__(ptc::NT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(v_tail));
         }
-    } else if (warp == W_MMA || warp == W_MMA + 1) {
-        // ------------------------------ MMA issuers: one thread per row tile ------------------------------
-        const int i = warp - W_MMA;
-        if (i < n_qt && lane == 0) {
-            constexpr uint32_t id_qk = idesc_bf16_f32(128, TB, false, false);
-            constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
-            constexpr int B4 = C::BOX >> 4;
-            const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + i * C::TILE), 16, 1024);
+    } else if (warp >= W_MMA && warp < W_MMA + 2 * n_qt) {
+        // ------------------------------ MMA issuers ------------------------------
+        const int i = (warp - W_MMA) / 2;
+        constexpr int B4 = C::BOX >> 4, T4 = C::TILE >> 4, H4 = TB * 128 >> 4;
+        const uint32_t ts = tmem + C::T_S + 2 * i * TB, to = tmem + C::T_O + i * D;
+        if (lane == 0 && (warp - W_MMA) % 2 == 0) {  // S_i(n) = Q_i K_n^T
+            constexpr uint32_t idesc = idesc_bf16_f32(128, TB, false, false);
+            const uint64_t qd = smem_desc_sw128(smem_u32(smem + i * C::TILE), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::OFF_RING), C::BOX, 1024);
-            const uint32_t ts = tmem + C::T_S + i * 2 * TB, to = tmem + C::T_O + i * D;
-            int ks = 0, vs = 1, kp = 0, vp = 0;  // ring stages of the current K and V tile, and their phases
-            auto step = [&](int& st, int& ph) {
-                st += 2;
-                if (st >= C::NS) {
-                    st -= C::NS;
-                    ph ^= 1;
-                }
-            };
-            auto scores = [&](int n) {  // S(n)
-                const uint64_t kd = k_desc + (uint64_t)(ks * (C::TILE >> 4) + (n & 1) * (TB * 128 >> 4));
+            bool ok = mbar_wait(smem_u32(q_full), 0, p.status);
+            for (int n = 0, st = 0, ph = 0; ok && n < nb; ++n) {
+                if (!(n & 1)) ok = mbar_wait(smem_u32(&full[st]), ph, p.status);
+                // the buffer's P has been read
+                if (ok && n >= 2) ok = mbar_wait(smem_u32(&o_ready[2 * i + (n & 1)]), ((n >> 1) - 1) & 1, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t kd = k_desc + (uint64_t)(st * T4 + (n & 1) * H4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_ss(ts + (n & 1) * TB, q_desc + (k / 4) * B4 + (k % 4) * 2, kd + (k / 4) * B4 + (k % 4) * 2, id_qk,
+                    umma_ss(ts + (n & 1) * TB, qd + (k / 4) * B4 + (k % 4) * 2, kd + (k / 4) * B4 + (k % 4) * 2, idesc,
                             k != 0);
                 umma_commit(smem_u32(&s_ready[2 * i + (n & 1)]));
                 if ((n & 1) || n == nb - 1) {
-                    umma_commit(smem_u32(&empty[ks]));
-                    step(ks, kp);
+                    umma_commit(smem_u32(&empty[st]));
+                    st += 2;
+                    if (st >= C::NS) {
+                        st -= C::NS;
+                        ph ^= 1;
+                    }
                 }
-            };
-            bool ok = mbar_wait(smem_u32(q_full), 0, p.status) && mbar_wait(smem_u32(&full[0]), 0, p.status);
-            if (ok) {
-                tc_fence_after();
-                scores(0);
-                if (nb > 1) scores(1);
             }
-            for (int n = 0; ok && n < nb; ++n) {
+            if (!ok) s_abort = 1;
+        } else if (lane == 0) {  // O_i += P_i(n) V_n
+            constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::OFF_RING), C::BOX, 1024);
+            bool ok = true;
+            for (int n = 0, st = 1, ph = 0; ok && n < nb; ++n) {
                 if (!(n & 1)) {
-                    ok = mbar_wait(smem_u32(&full[vs]), vp, p.status);
+                    ok = mbar_wait(smem_u32(&full[st]), ph, p.status);
                     if (ok && kend - (kbeg + n * TB) < TK) ok = mbar_wait(smem_u32(v_tail), 0, p.status);
-                    if (ok && n + 2 < nb) ok = mbar_wait(smem_u32(&full[ks]), kp, p.status);
                 }
                 if (ok) ok = mbar_wait(smem_u32(&p_ready[2 * i + (n & 1)]), (n >> 1) & 1, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t vd = v_desc + (uint64_t)(vs * (C::TILE >> 4) + (n & 1) * (TB * 128 >> 4));
+                const uint64_t vd = v_desc + (uint64_t)(st * T4 + (n & 1) * H4);
 #pragma unroll
                 for (int k = 0; k < TB / 16; ++k)
-                    umma_ts(to, ts + (n & 1) * TB + k * 8, vd + k * (2048 >> 4), id_pv, (n | k) != 0);
-                umma_commit(smem_u32(&o_ready[i]));
+                    umma_ts(to, ts + (n & 1) * TB + k * 8, vd + k * (2048 >> 4), idesc, (n | k) != 0);
+                umma_commit(smem_u32(&o_ready[2 * i + (n & 1)]));
                 if (n == nb - 1) umma_commit(smem_u32(&o_done[i]));
-                if (n + 2 < nb) scores(n + 2);
                 if ((n & 1) || n == nb - 1) {
-                    umma_commit(smem_u32(&empty[vs]));
-                    step(vs, vp);
+                    umma_commit(smem_u32(&empty[st]));
+                    st += 2;
+                    if (st >= C::NS) {
+                        st -= C::NS;
+                        ph ^= 1;
+                    }
                 }
             }
             if (!ok) s_abort = 1;
@@ -273,8 +274,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                 l2.x *= alpha;
                 l2.y *= alpha;
                 if (n > 0) {
-                    // O has to hold block n - 1; s_ready(n) told that it holds n - 2, and n waits for this warp
-                    if (ok) ok = mbar_wait(smem_u32(&o_ready[i]), (n - 1) & 1, p.status);
+                    // O has to hold block n - 1 (block n waits for this warp, and n - 2 was in before S(n))
+                    if (ok) ok = mbar_wait(smem_u32(&o_ready[2 * i + ((n - 1) & 1)]), ((n - 1) >> 1) & 1, p.status);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
