@@ -5,18 +5,20 @@
 // One CTA takes two tiles of up to 128 query rows of one KV head and a range of the
 // prefix's keys; the two row tiles share every K and V tile of 128 keys, which warp 8 streams
 // with TMA through one ring.  Scores are made 64 keys at a time into two buffers per row tile:
-// one thread of warp 9 + i issues the MMAs of row tile i, per block n: O_i += P_i(n) V_n, then
-// S_i(n + 2) = Q_i K_{n+2}^T; warps 0-3 and 4-7 are the softmax of row tile 0 and 1, one
-// thread per row, which finds S_i(n + 1) made while it works on block n.  P_i(n) overwrites
-// S_i(n) in tensor memory: MMAs of one thread run in the order they are issued, so S_i(n + 2)
-// follows the P V product that reads P_i(n).
+// warps 0-3 and 4-7 are the softmax of row tile 0 and 1, one thread per row, and find the next
+// block of scores made while they work on this one.  P_i(n), in bf16, overwrites S_i(n) in
+// tensor memory.  Four threads issue the MMAs, two per row tile (scores; values), each waiting
+// only for what its product needs, so that one's waits (about 200 cycles each) pass under the
+// others' MMAs; the tensor core's reads of P_i(n) and writes of S_i(n + 2) are ordered by a commit.
 //
-// Bound: per 128 keys the 2 x 128 x 128 x 4 d FLOPs take 2576 tensor cycles at d = 128 (2080
-// at the full rate; an N = 64 MMA costs 48 cycles, not 32) and 32,768 exponentials 2048 cycles
-// of the special-function unit (16 per cycle and SM).  One score buffer of 128 keys per row
-// tile ran at 5000 cycles: the chain score product, softmax, value product of each row tile was
-// then serial, and the two row tiles fell into step.  Below about 256 rows per KV head the
-// prefix's bytes bound.
+// Bound: per 128 keys the 2 x 128 x 128 x 4 d FLOPs take 2640 tensor cycles at d = 128 (2080
+// at the full rate; an N = 64 MMA costs 50 cycles, not 32) and 32,768 exponentials 2048 cycles
+// of the special-function unit (16 per cycle and SM).  Measured on 256 sequences of 2 queries,
+// 32 / 8 heads of 128, a paged prefix of 16,384 keys (137 GFLOP): 132 us, 0.61 of the measured
+// dense rate.  Steps to it: one score buffer of 128 keys per row tile and one issuing thread
+// 193 us (score product, softmax, value product in series); 64-key blocks 171; four issuing
+// threads 176 but ordered; the row tiles taking turns at the exponentials 175; one lane per TMA
+// box with its page looked up early 132 (one lane alone took 1500 cycles per tile).
 #include <math.h>
 
 #include <algorithm>
@@ -46,6 +48,10 @@ struct Cfg {
 };
 }  // namespace ptc
 
+__device__ __forceinline__ void named_barrier_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(ptc::NT, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -64,7 +70,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     uint64_t* o_done = o_ready + 4;     // [2]
     uint64_t* v_tail = o_done + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_tail + 1);
-    __shared__ int s_abort, s_loaded;
+    __shared__ int s_abort;
 
     const int pairs = cdiv(g.n_tiles, 2);
     const int pair = blockIdx.x % pairs, split = (blockIdx.x / pairs) % p.n_pre, kvh = blockIdx.x / (pairs * p.n_pre);
@@ -77,7 +83,6 @@ __global__ void __launch_bounds__(ptc::NT, 1)
 
     if (threadIdx.x == 0) {
         s_abort = 0;
-        s_loaded = 0;
         mbar_init(smem_u32(q_full), 1);
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
@@ -105,8 +110,10 @@ __global__ void __launch_bounds__(ptc::NT, 1)
 
     if (warp == W_LOAD) {
         // ------------------------------ producer: Q, then K_0, V_0, K_1, V_1, ... ------------------------------
+        // One lane per box of a tile (a tile is one box, or one per page piece); the rows of tile j + 1 are looked up
+        // while its ring stage is still in use, once for its keys and values.
+        const uint32_t qb = smem_u32(q_full);
         if (lane == 0) {
-            const uint32_t qb = smem_u32(q_full);
             mbar_arrive_expect_tx(qb, n_qt * C::NB * g.rows * 128);
             for (int i = 0; i < n_qt; ++i) {
                 const int t = 2 * pair + i;
@@ -115,48 +122,50 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                 for (int x = 0; x < C::NB; ++x)
                     tma_load_4d(smem_u32(smem + i * C::TILE + x * C::BOX), &tm_q, x * 64, g0, kvh, b0, qb);
             }
-            bool ok = true;
-            int issued = 0;
-            for (int n = 0; n < 2 * n_kt; ++n) {
-                const int s = n % C::NS;
-                if (*(volatile int*)&s_abort) break;
-                if (n >= C::NS && !mbar_wait(smem_u32(&empty[s]), (n / C::NS - 1) & 1, p.status)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + C::OFF_RING + s * C::TILE);
-                mbar_arrive_expect_tx(fb, C::TILE);
-                const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
-                for (int r = 0; r < TK; r += g.box_rows) {
-                    const int tok = kbeg + n / 2 * TK + r;
-                    int y = tok, z = kvh;
-                    if (p.ptable) {
-                        // pages [num_pages][h_kv][page_size]; rows past the keys of this split are not looked up
-                        int page = tok < kend ? p.ptable[tok / p.page_size] : 0;
-                        if (page < 0 || page >= p.num_pages) {
-                            atomicOr(p.status, kDevBadPage);
-                            page = 0;
-                        }
-                        y = tok % p.page_size;
-                        z = page * p.h_kv + kvh;
-                    }
-#pragma unroll
-                    for (int x = 0; x < C::NB; ++x) tma_load_3d(dst + x * C::BOX + r * 128, map, x * 64, y, z, fb);
-                }
-                ++issued;
-            }
-            if (!ok) s_abort = 1;
-            // every issued copy lands before the CTA may end
-            for (int n = issued - 1; n >= 0 && n >= issued - C::NS; --n)
-                mbar_wait(smem_u32(&full[n % C::NS]), (n / C::NS) & 1, p.status);
-            mbar_wait(qb, 0, p.status);
-            *(volatile int*)&s_loaded = issued;
         }
-        __syncwarp();
-        const int n = 2 * n_kt - 1, valid = kend - (kbeg + n / 2 * TK);
-        if (valid < TK && *(volatile int*)&s_loaded == 2 * n_kt) {
-            // the last tile's value rows past the keys may hold anything, and 0 x NaN would reach every row: zeros
+        const int r = lane * g.box_rows;
+        int y = 0, z = kvh;
+        auto look_up = [&](int j) {
+            const int tok = kbeg + j * TK + r;
+            if (r >= TK) return;
+            y = tok;
+            if (p.ptable) {
+                // pages [num_pages][h_kv][page_size]; rows past the keys of this split are not looked up
+                int page = tok < kend ? p.ptable[tok / p.page_size] : 0;
+                if (page < 0 || page >= p.num_pages) {
+                    atomicOr(p.status, kDevBadPage);
+                    page = 0;
+                }
+                y = tok % p.page_size;
+                z = page * p.h_kv + kvh;
+            }
+        };
+        look_up(0);
+        int issued = 0;
+        bool ok = true;
+        for (int n = 0; n < 2 * n_kt; ++n) {
+            const int s = n % C::NS;
+            if (n >= C::NS) ok = mbar_wait(smem_u32(&empty[s]), (n / C::NS - 1) & 1, p.status);
+            if (!__all_sync(0xffffffffu, ok && !*(volatile int*)&s_abort)) break;
+            const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + C::OFF_RING + s * C::TILE) + r * 128;
+            if (lane == 0) mbar_arrive_expect_tx(fb, C::TILE);
+            __syncwarp();
+            if (r < TK) {
+                const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
+#pragma unroll
+                for (int x = 0; x < C::NB; ++x) tma_load_3d(dst + x * C::BOX, map, x * 64, y, z, fb);
+            }
+            ++issued;
+            if (n & 1) look_up(n / 2 + 1);
+        }
+        if (!ok) s_abort = 1;
+        // every issued copy lands before the CTA may end
+        for (int n = issued - 1; n >= 0 && n >= issued - C::NS; --n)
             mbar_wait(smem_u32(&full[n % C::NS]), (n / C::NS) & 1, p.status);
+        mbar_wait(qb, 0, p.status);
+        const int n = 2 * n_kt - 1, valid = kend - (kbeg + n / 2 * TK);
+        if (valid < TK && issued == 2 * n_kt) {
+            // the last tile's value rows past the keys may hold anything, and 0 x NaN would reach every row: zeros
             uint8_t* v = smem + C::OFF_RING + n % C::NS * C::TILE;
             const int rows = TK - valid;
             for (int x = lane; x < C::NB * rows * 8; x += 32)
@@ -235,6 +244,10 @@ __global__ void __launch_bounds__(ptc::NT, 1)
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
+        // The two warps of an SM sub-partition (one of each row tile) take turns at the exponentials: left alone they
+        // fall into step, contend for the special-function unit and then leave it idle together.
+        const int bar_mine = 1 + 2 * (warp % 4) + i, bar_other = 1 + 2 * (warp % 4) + (i ^ 1);
+        if (n_qt == 2 && i == 1) named_barrier_arrive(bar_other, 64);  // row tile 0 goes first
         for (int n = 0; n < nb; ++n) {
             const uint32_t ts = tmem + lanes + C::T_S + (2 * i + (n & 1)) * TB;
             if (ok) ok = mbar_wait(smem_u32(&s_ready[2 * i + (n & 1)]), (n >> 1) & 1, p.status);
@@ -288,6 +301,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                     }
                 }
             }
+            if (n_qt == 2) named_barrier(bar_mine, 64);
             const float ms = m == -INFINITY ? 0.f : m;
             const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-ms, -ms);
             float2 part[2] = {l2, make_float2(0.f, 0.f)};
@@ -304,6 +318,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                 tmem_st16(ts + 16 * h, pk);
             }
             l2 = __fadd2_rn(part[0], part[1]);
+            if (n_qt == 2 && (i == 0 || n + 1 < nb)) named_barrier_arrive(bar_other, 64);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
