@@ -39,9 +39,12 @@ struct Work {
     int L;             // length of the key sequence
 };
 
-// Item `idx` of the grid; false: nothing to do.
-__device__ __forceinline__ bool find_work(const PrefixParams& p, int rows_per_block, Work& w, bool report) {
-    int idx = blockIdx.x;
+// Items of a launch, and item `idx` of them; false: nothing to do.
+__host__ __device__ inline long long count_work(const PrefixParams& p, int rows_per_block) {
+    return (p.do_prefix ? (long long)cdiv(p.B * p.R, rows_per_block) * p.h_kv * p.n_pre : 0) +
+           (p.do_suffix ? (long long)p.B * p.h_kv * cdiv(p.R, rows_per_block) * p.n_suf : 0);
+}
+__device__ __forceinline__ bool find_work(const PrefixParams& p, int rows_per_block, int idx, Work& w, bool report) {
     const int rb_pre = cdiv(p.B * p.R, rows_per_block), n_pre_items = p.do_prefix ? rb_pre * p.h_kv * p.n_pre : 0;
     if (idx < n_pre_items) {
         // row blocks of one (head, split) are neighbours: they read the same keys
@@ -102,17 +105,371 @@ __device__ __forceinline__ CacheRows rows_of(const PrefixParams& p, const Work& 
 }
 
 // ---- bf16: warp-level MMAs ------------------------------------------------------------------------------------
-// ROWS4 = false: 16 query rows; the four warps take 16 keys each of a 64-key tile and join their states at the end.
-// ROWS4 = true: 64 query rows, 16 per warp, every warp takes the whole tile.
-template <int D, bool ROWS4>
-struct MmaCfg {
-    static constexpr int TK = 64, ROWS = ROWS4 ? 64 : 16;
-    static constexpr int KG = ROWS4 ? 4 : 1;            // 16-key groups of a tile per warp
-    static constexpr int STAGES = D == 64 ? 4 : 3;
+// What both kernels do with 16 query rows and KG groups of 16 keys: scores, online softmax, values.  A warp's lane
+// (g, t) holds rows g and g + 8.
+template <int D>
+struct RowState {
+    float o[D / 8][4];
+    float m[2], l[2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+    // the row sums over the four lanes of a row
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+    }
+};
+
+// q(ks, regs): A fragments of k-step ks; k_at / v_at (row, 16-byte chunk): shared addresses of the tile; the warp's
+// keys are rows key_w .. of the tile, key k0 + j the j-th of them; keys below vis[h] are visible to row g + 8 h.
+template <int D, int KG, class Q, class KA, class VA>
+__device__ __forceinline__ void attend_tile(RowState<D>& st, const Q& q, const KA& k_at, const VA& v_at, int key_w, int k0,
+                                            const int* vis, int vis_all, float scale_log2) {
+    const int lane = threadIdx.x % 32, t = lane % 4;
+    float s[KG][2][4];
+#pragma unroll
+    for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) s[kg][n][0] = s[kg][n][1] = s[kg][n][2] = s[kg][n][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t qa[4];
+        q(ks, qa);
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+            uint32_t kf[4];  // matrices: (keys 0-7, k 0-7), (keys 0-7, k 8-15), (keys 8-15, ..) x 2
+            ldmatrix4(kf, k_at(key_w + kg * 16 + (lane / 16) * 8 + lane % 8, 2 * ks + (lane / 8) % 2));
+            mma_bf16(s[kg][0], qa, kf[0], kf[1]);
+            mma_bf16(s[kg][1], qa, kf[2], kf[3]);
+        }
+    }
+    float mx[2] = {-INFINITY, -INFINITY};
+    const bool whole = k0 + 16 * KG <= vis_all;
+#pragma unroll
+    for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = s[kg][n][e] * scale_log2;
+                if (!whole && k0 + kg * 16 + n * 8 + 2 * t + (e & 1) >= vis[e / 2]) x = -INFINITY;
+                s[kg][n][e] = x;
+                mx[e / 2] = fmaxf(mx[e / 2], x);
+            }
+    // the reference maximum moves only when a score exceeds it by 2^8; a row's lanes agree on it only then
+    const bool grow = mx[0] > st.m[0] + 8.f || mx[1] > st.m[1] + 8.f || (st.m[0] == -INFINITY && mx[0] > -INFINITY) ||
+                      (st.m[1] == -INFINITY && mx[1] > -INFINITY);
+    if (__any_sync(0xffffffffu, grow)) {
+        float al[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            // by its own row alone: what other rows (or rows past the item) hold changes nothing
+            const bool move = mx[h] > st.m[h] + 8.f || (st.m[h] == -INFINITY && mx[h] > -INFINITY);
+            al[h] = move ? fast_exp2(st.m[h] - mx[h]) : 1.f;
+            if (move) st.m[h] = mx[h];
+            st.l[h] *= al[h];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            st.o[i][0] *= al[0];
+            st.o[i][1] *= al[0];
+            st.o[i][2] *= al[1];
+            st.o[i][3] *= al[1];
+        }
+    }
+    const float ms[2] = {st.m[0] == -INFINITY ? 0.f : st.m[0], st.m[1] == -INFINITY ? 0.f : st.m[1]};
+    // P in the A layout of the value product (rounded to bf16 as everywhere in the library; the sums are of the fp32
+    // values)
+#pragma unroll
+    for (int kg = 0; kg < KG; ++kg) {
+        uint32_t pa[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = fast_exp2(s[kg][n][i] - ms[i / 2]);
+            st.l[0] += e[0] + e[1];
+            st.l[1] += e[2] + e[3];
+            pa[2 * n] = bf16_pair(e[0], e[1]);
+            pa[2 * n + 1] = bf16_pair(e[2], e[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            uint32_t vf[4];  // transposed: (keys 0-7, 8-15) of value columns 16 i .. + 7, then .. + 15
+            ldmatrix4_t(vf, v_at(key_w + kg * 16 + lane % 16, 2 * i + lane / 16));
+            mma_bf16(st.o[2 * i], pa, vf[0], vf[1]);
+            mma_bf16(st.o[2 * i + 1], pa, vf[2], vf[3]);
+        }
+    }
+}
+
+// Few rows: 16 query rows per item, the four consumer warps take 16 keys each of a 64-key tile and join their states
+// at the end of the item.  Bound by reading K and V (a suffix's are read once), so the blocks are persistent: warp 4
+// streams the tiles of one item after another with TMA through one ring, which never drains between items, and hands
+// the consumers each item's description with its query rows.
+template <int D>
+struct StreamCfg {
+    static constexpr int TK = 64, ROWS = 16, NB = D / 64;
+    static constexpr int BOX = TK * 128, MAT = NB * BOX, STAGE = 2 * MAT;  // a box: 64 rows of 64 values
+    static constexpr int NS = D == 64 ? 4 : 3;
+    static constexpr int BLOCKS = D == 64 ? 3 : D == 128 ? 2 : 1;          // per SM
+    static constexpr int QROW = D * 2 + 16;                                // padded: ldmatrix without bank conflicts
+    static constexpr int OFF_Q = NS * STAGE, OFF_O = OFF_Q + ROWS * QROW;  // O: [16][D] fp32, the join
+    static constexpr int OFF_ML = OFF_O + ROWS * D * 4;                    // [4][16] maxima, then sums
+    static constexpr int OFF_BAR = OFF_ML + 2 * 4 * ROWS * 4;
+    static constexpr int SMEM = 1024 + OFF_BAR + 128;
+    static_assert((SMEM + 1024) * BLOCKS <= 233472, "shared memory");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
+    prefix_stream_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
+                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const PrefixParams p, const int n_items, const int box_rows) {
+    using C = StreamCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(smem_raw), 1024));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + C::NS;
+    uint64_t* q_full = empty + C::NS;
+    uint64_t* q_empty = q_full + 1;
+    __shared__ Work s_work;
+    __shared__ int s_more, s_abort;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 4);
+        }
+        mbar_init(smem_u32(q_full), 1);
+        mbar_init(smem_u32(q_empty), 4);
+        fence_barrier_init();
+    }
+    __syncthreads();
+
+    if (warp == 4) {
+        // ------------------------------ producer: one lane per box of a tile ------------------------------
+        const int r = lane * box_rows;
+        int n = 0, item = 0;  // tiles and items issued
+        bool ok = true;
+        auto next_item = [&](const Work* w) {  // hands over an item, or the end
+            if (item > 0) ok = mbar_wait(smem_u32(q_empty), (item - 1) & 1, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            const uint32_t qb = smem_u32(q_full);
+            if (lane == 0) {
+                s_more = w && ok;
+                if (w) s_work = *w;
+                __threadfence_block();
+                if (w && ok)
+                    mbar_arrive_expect_tx(qb, w->nrows * D * 2);
+                else
+                    mbar_arrive(qb);
+            }
+            __syncwarp();
+            if (w && ok && lane < w->nrows)
+                bulk_load(smem_u32(smem + C::OFF_Q) + lane * C::QROW,
+                          static_cast<const __nv_bfloat16*>(p.q) + global_row(p, *w, lane) * D, D * 2, qb);
+            ++item;
+        };
+        for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+            Work w;
+            if (!find_work(p, C::ROWS, idx, w, lane == 0)) continue;
+            next_item(&w);
+            const CUtensorMap* mk = w.prefix ? &tm_kp : &tm_k;
+            const CUtensorMap* mv = w.prefix ? &tm_vp : &tm_v;
+            const int32_t* table = p.table ? (w.prefix ? p.ptable : p.table + (size_t)w.b * p.max_pages) : nullptr;
+            int y = 0, z = w.prefix ? w.kvh : w.b * p.h_kv + w.kvh;
+            auto look_up = [&](int tile) {
+                const int tok = w.kbeg + tile * C::TK + r;
+                y = tok;
+                if (table) {
+                    int page = r < C::TK && tok < w.kend ? table[tok / p.page_size] : 0;
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicOr(p.status, kDevBadPage);
+                        page = 0;
+                    }
+                    y = tok % p.page_size;
+                    z = page * p.h_kv + w.kvh;
+                }
+            };
+            look_up(0);
+            const int n_tiles = cdiv(w.kend - w.kbeg, C::TK);
+            for (int j = 0; ok && j < n_tiles; ++j, ++n) {
+                const int s = n % C::NS;
+                if (n >= C::NS) ok = mbar_wait(smem_u32(&empty[s]), (n / C::NS - 1) & 1, p.status);
+                ok = __all_sync(0xffffffffu, ok && !*(volatile int*)&s_abort);
+                if (!ok) break;
+                const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * C::STAGE) + r * 128;
+                if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
+                __syncwarp();
+                if (r < C::TK) {
+#pragma unroll
+                    for (int x = 0; x < C::NB; ++x) {
+                        tma_box(dst + x * C::BOX, mk, x * 64, y, z, fb);
+                        tma_box(dst + C::MAT + x * C::BOX, mv, x * 64, y, z, fb);
+                    }
+                }
+                if (j + 1 < n_tiles) look_up(j + 1);
+            }
+        }
+        next_item(nullptr);
+        // every issued copy lands before the CTA may end
+        for (int i = n - 1; i >= 0 && i >= n - C::NS; --i)
+            mbar_wait(smem_u32(&full[i % C::NS]), (i / C::NS) & 1, p.status);
+        return;
+    }
+
+    const int g = lane / 4, t = lane % 4, key_w = warp * 16;
+    float* om = reinterpret_cast<float*>(smem + C::OFF_O);
+    float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+    const uint32_t sq = smem_u32(smem + C::OFF_Q);
+    RowState<D> st;
+    int n = 0;
+    for (int item = 0;; ++item) {
+        bool ok = mbar_wait(smem_u32(q_full), item & 1, p.status);
+        if (!ok || !s_more) {
+            if (!ok) s_abort = 1;
+            break;
+        }
+        const Work w = s_work;
+        constexpr bool QREG = D <= 128;  // the query fragments stay in registers; otherwise they are read again per tile
+        uint32_t qf[QREG ? D / 16 : 1][4];
+        auto q_at = [&](int ks, uint32_t* to) { ldmatrix4(to, sq + (lane % 16) * C::QROW + (2 * ks + lane / 16) * 16); };
+        if constexpr (QREG) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) q_at(ks, qf[ks]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(q_empty));
+        }
+        int vis[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h;
+            vis[h] = r < w.nrows ? min(visible_end(p, w, r), w.kend) : 0;
+        }
+        // keys below are visible to every row of the item (rows past it do not count)
+        const int vis_all = __reduce_min_sync(0xffffffffu, min(g < w.nrows ? vis[0] : w.kend, g + 8 < w.nrows ? vis[1] : w.kend));
+        st.clear();
+        const int n_tiles = cdiv(w.kend - w.kbeg, C::TK);
+        for (int j = 0; j < n_tiles; ++j, ++n) {
+            const int s = n % C::NS;
+            if (ok) ok = mbar_wait(smem_u32(&full[s]), (n / C::NS) & 1, p.status);
+            const int k0 = w.kbeg + j * C::TK + key_w;
+            if (ok && k0 < w.kend) {
+                uint8_t* kt = smem + s * C::STAGE;
+                const uint32_t kb = smem_u32(kt), vb = kb + C::MAT;
+                auto at = [](uint32_t base, int r, int c) { return base + (c / 8) * C::BOX + r * 128 + (((c % 8) ^ (r & 7)) * 16); };
+                if (k0 + 16 > w.kend) {
+                    // value rows past the keys may hold anything, and 0 x NaN would reach every row: zeros
+                    const int first = w.kend - k0;
+                    for (int x = lane; x < (16 - first) * (D / 8); x += 32) {
+                        const int r = key_w + first + x / (D / 8), c = x % (D / 8);
+                        *reinterpret_cast<uint4*>(kt + C::MAT + (c / 8) * C::BOX + r * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into the stage
+                    __syncwarp();
+                }
+                auto q_regs = [&](int ks, uint32_t* to) {
+                    if constexpr (QREG) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) to[e] = qf[ks][e];
+                    } else {
+                        q_at(ks, to);
+                    }
+                };
+                attend_tile<D, 1>(st, q_regs, [&](int r, int c) { return at(kb, r, c); }, [&](int r, int c) { return at(vb, r, c); },
+                                  key_w, k0, vis, vis_all, p.scale_log2);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
+        }
+        if constexpr (!QREG) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(q_empty));
+        }
+        // join the four warps' states, one after the other into one buffer
+        st.finish();
+        if (t == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ml[warp * 16 + g + 8 * h] = st.m[h];
+                ml[64 + warp * 16 + g + 8 * h] = st.l[h];
+            }
+        }
+        named_barrier(1, 128);
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h;
+            const float M = fmaxf(fmaxf(ml[r], ml[16 + r]), fmaxf(ml[32 + r], ml[48 + r]));
+            f[h] = M == -INFINITY ? 0.f : fast_exp2(st.m[h] - M);
+        }
+        for (int k = 0; k < 4; ++k) {
+            if (k == warp) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = g + 8 * h;
+                    if (r >= w.nrows) continue;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        float2* x = reinterpret_cast<float2*>(om + r * D + i * 8 + 2 * t);
+                        float2 v = make_float2(st.o[i][2 * h] * f[h], st.o[i][2 * h + 1] * f[h]);
+                        if (k) v = __fadd2_rn(v, *x);
+                        *x = v;
+                    }
+                }
+            }
+            named_barrier(1, 128);
+        }
+        for (int i = threadIdx.x; i < w.nrows * (D / 4); i += 128) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            float M = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) M = fmaxf(M, ml[k * 16 + r]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum += M == -INFINITY ? 0.f : fast_exp2(ml[k * 16 + r] - M) * ml[64 + k * 16 + r];
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float4 x = *reinterpret_cast<const float4*>(om + r * D + c * 4);
+            const size_t to = global_row(p, w, r) * p.n_slots + w.slot;
+            *reinterpret_cast<float4*>(p.part_o + to * D + c * 4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            if (c == 0) p.part_lse[to] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+        }
+        named_barrier(1, 128);  // the buffers are free for the next item
+        if (!ok) s_abort = 1;
+    }
+}
+
+// Many rows at d = 256 (whose accumulators do not fit prefix_tc_kernel's tensor memory twice): 64 query rows, 16 per
+// warp, every warp takes whole tiles of 64 keys, copied row by row.
+template <int D>
+struct Rows64Cfg {
+    static constexpr int TK = 64, ROWS = 64, STAGES = 3;
     static constexpr int MAT = TK * D * 2, STAGE = 2 * MAT, QB = ROWS * D * 2;
     static constexpr int SMEM = QB + STAGES * STAGE;
-    // the merge of four warps' states reuses the stages: [4][16][D] fp32
-    static_assert(ROWS4 || 4 * 16 * D * 4 + 2 * 4 * 16 * 4 <= STAGES * STAGE, "merge scratch");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -123,18 +480,17 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
     return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) * 16));
 }
 
-template <int D, bool ROWS4>
-__global__ void __launch_bounds__(128) prefix_mma_kernel(const PrefixParams p) {
-    using C = MmaCfg<D, ROWS4>;
+template <int D>
+__global__ void __launch_bounds__(128) prefix_rows64_kernel(const PrefixParams p) {
+    using C = Rows64Cfg<D>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     Work w;
-    if (!find_work(p, C::ROWS, w, tid == 0)) return;
+    if (!find_work(p, C::ROWS, blockIdx.x, w, tid == 0)) return;
     const CacheRows rows = rows_of(p, w);
     const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(w.prefix ? p.kp : p.k);
     const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(w.prefix ? p.vp : p.v);
     const uint32_t sq = smem_u32(smem), st0 = sq + C::QB;
-
     for (int i = tid; i < C::ROWS * (D / 8); i += 128) {
         const int r = i / (D / 8), c = i % (D / 8);
         const bool ok = r < w.nrows;
@@ -160,9 +516,7 @@ __global__ void __launch_bounds__(128) prefix_mma_kernel(const PrefixParams p) {
         if (s < n_tiles) load_tile(s, s);
         cp_async_commit();
     }
-
-    const int row_w = ROWS4 ? warp * 16 : 0, key_w = ROWS4 ? 0 : warp * 16;
-    // this lane's rows are g and g + 8 of the warp's 16
+    const int row_w = warp * 16;
     int vis[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -170,164 +524,31 @@ __global__ void __launch_bounds__(128) prefix_mma_kernel(const PrefixParams p) {
         vis[h] = r < w.nrows ? min(visible_end(p, w, r), w.kend) : 0;
     }
     const int vis_all = __reduce_min_sync(0xffffffffu, min(vis[0], vis[1]));
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    constexpr bool QREG = D <= 128;  // the query fragments stay in registers
-    uint32_t qf[QREG ? D / 16 : 1][4];
-    const int arow = lane % 16, acol = lane / 16;  // ldmatrix addresses of a 16 x 16 A operand
-
+    RowState<D> st;
+    st.clear();
     for (int j = 0; j < n_tiles; ++j) {
         cp_async_wait<C::STAGES - 2>();
         __syncthreads();
         if (j + C::STAGES - 1 < n_tiles) load_tile(j + C::STAGES - 1, (j + C::STAGES - 1) % C::STAGES);
         cp_async_commit();
-        if constexpr (QREG) {
-            if (j == 0) {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) ldmatrix4(qf[ks], sq + swz<D>(row_w + arow, 2 * ks + acol));
-            }
-        }
         const uint32_t kt = st0 + (j % C::STAGES) * C::STAGE, vt = kt + C::MAT;
-        const int k0 = w.kbeg + j * C::TK + key_w;
-        // scores: KG groups of 16 keys, two 8-key column blocks each
-        float s[C::KG][2][4];
-#pragma unroll
-        for (int kg = 0; kg < C::KG; ++kg)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) s[kg][n][0] = s[kg][n][1] = s[kg][n][2] = s[kg][n][3] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t qa[4];
-            if constexpr (!QREG) ldmatrix4(qa, sq + swz<D>(row_w + arow, 2 * ks + acol));
-#pragma unroll
-            for (int kg = 0; kg < C::KG; ++kg) {
-                uint32_t kf[4];  // matrices: (keys 0-7, k 0-7), (keys 0-7, k 8-15), (keys 8-15, ..) x 2
-                ldmatrix4(kf, kt + swz<D>(key_w + kg * 16 + (lane / 16) * 8 + lane % 8, 2 * ks + (lane / 8) % 2));
-                mma_bf16(s[kg][0], QREG ? qf[QREG ? ks : 0] : qa, kf[0], kf[1]);
-                mma_bf16(s[kg][1], QREG ? qf[QREG ? ks : 0] : qa, kf[2], kf[3]);
-            }
-        }
-        // mask, running maximum
-        float mx[2] = {-INFINITY, -INFINITY};
-        const bool whole = k0 + 16 * C::KG <= vis_all;
-#pragma unroll
-        for (int kg = 0; kg < C::KG; ++kg)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = s[kg][n][e] * p.scale_log2;
-                    if (!whole && k0 + kg * 16 + n * 8 + 2 * t + (e & 1) >= vis[e / 2]) x = -INFINITY;
-                    s[kg][n][e] = x;
-                    mx[e / 2] = fmaxf(mx[e / 2], x);
-                }
-        bool grow = false;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-            grow |= mx[h] > m[h];
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-            float al[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float mn = fmaxf(m[h], mx[h]);
-                al[h] = mn == -INFINITY ? 1.f : fast_exp2(m[h] - mn);
-                m[h] = mn;
-                l[h] *= al[h];
-            }
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                o[i][0] *= al[0];
-                o[i][1] *= al[0];
-                o[i][2] *= al[1];
-                o[i][3] *= al[1];
-            }
-        }
-        const float ms[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-        // P in the A layout of the value product (rounded to bf16 as everywhere in the library; the sums are of
-        // the fp32 values)
-#pragma unroll
-        for (int kg = 0; kg < C::KG; ++kg) {
-            uint32_t pa[4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                float e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = fast_exp2(s[kg][n][i] - ms[i / 2]);
-                l[0] += e[0] + e[1];
-                l[1] += e[2] + e[3];
-                pa[2 * n] = bf16_pair(e[0], e[1]);
-                pa[2 * n + 1] = bf16_pair(e[2], e[3]);
-            }
-            const int vrow = key_w + kg * 16 + lane % 16;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t vf[4];  // transposed: (keys 0-7, 8-15) of value columns 16 i .. + 7, then .. + 15
-                ldmatrix4_t(vf, vt + swz<D>(vrow, 2 * i + lane / 16));
-                mma_bf16(o[2 * i], pa, vf[0], vf[1]);
-                mma_bf16(o[2 * i + 1], pa, vf[2], vf[3]);
-            }
-        }
+        attend_tile<D, 4>(st, [&](int ks, uint32_t* to) { ldmatrix4(to, sq + swz<D>(row_w + lane % 16, 2 * ks + lane / 16)); },
+                          [&](int r, int c) { return kt + swz<D>(r, c); }, [&](int r, int c) { return vt + swz<D>(r, c); }, 0,
+                          w.kbeg + j * C::TK, vis, vis_all, p.scale_log2);
     }
     cp_async_wait<0>();
+    st.finish();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    }
-    if constexpr (ROWS4) {
+        const int r = row_w + g + 8 * h;
+        if (r >= w.nrows) continue;
+        const size_t at = global_row(p, w, r) * p.n_slots + w.slot;
+        const float inv = st.l[h] > 0.f ? 1.f / st.l[h] : 0.f;
+        float* po = p.part_o + at * D;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = row_w + g + 8 * h;
-            if (r >= w.nrows) continue;
-            const size_t at = global_row(p, w, r) * p.n_slots + w.slot;
-            const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
-            float* po = p.part_o + at * D;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(po + i * 8 + 2 * t) = make_float2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
-            if (t == 0) p.part_lse[at] = l[h] > 0.f ? m[h] + log2f(l[h]) : -INFINITY;
-        }
-    } else {
-        __syncthreads();
-        float* om = reinterpret_cast<float*>(smem + C::QB);  // [4][16][D]
-        float* mm = om + 4 * 16 * D;                         // [4][16] maxima, then sums
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = warp * 16 + g + 8 * h;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2*>(om + r * D + i * 8 + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
-            if (t == 0) {
-                mm[r] = m[h];
-                mm[64 + r] = l[h];
-            }
-        }
-        __syncthreads();
-        for (int i = tid; i < w.nrows * (D / 4); i += 128) {
-            const int r = i / (D / 4), c = i % (D / 4);
-            float M = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) M = fmaxf(M, mm[k * 16 + r]);
-            float sum = 0.f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float f = M == -INFINITY ? 0.f : fast_exp2(mm[k * 16 + r] - M);
-                const float4 x = *reinterpret_cast<const float4*>(om + (k * 16 + r) * D + c * 4);
-                sum += f * mm[64 + k * 16 + r];
-                a = make_float4(fmaf(f, x.x, a.x), fmaf(f, x.y, a.y), fmaf(f, x.z, a.z), fmaf(f, x.w, a.w));
-            }
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const size_t at = global_row(p, w, r) * p.n_slots + w.slot;
-            *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) =
-                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-            if (c == 0) p.part_lse[at] = sum > 0.f ? M + log2f(sum) : -INFINITY;
-        }
+        for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<float2*>(po + i * 8 + 2 * t) = make_float2(st.o[i][2 * h] * inv, st.o[i][2 * h + 1] * inv);
+        if (t == 0) p.part_lse[at] = st.l[h] > 0.f ? st.m[h] + log2f(st.l[h]) : -INFINITY;
     }
 }
 
@@ -350,7 +571,7 @@ __global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
     float* ps = vs + C::TK * D;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     Work w;
-    if (!find_work(p, C::ROWS, w, tid == 0)) return;
+    if (!find_work(p, C::ROWS, blockIdx.x, w, tid == 0)) return;
     const CacheRows rows = rows_of(p, w);
     const float* kb = static_cast<const float*>(w.prefix ? p.kp : p.k);
     const float* vb = static_cast<const float*>(w.prefix ? p.vp : p.v);
@@ -545,9 +766,8 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     if ((long long)B * h_q * s >= (1ll << 28) || Lp > (1 << 30) || Lmax > (1 << 30)) return LKA_ERR_UNSUPPORTED;
     const int R = h_q / h_kv * s, Bn = std::max(B, 1);
     const bool f32 = dtype == LKA_FP32;
-    // Up to 16 query rows per KV head in all, warps split the keys of prefix_mma_kernel.  More, and the head dim fits
-    // prefix_tc_kernel's tensor memory: that one.  d = 256: prefix_mma_kernel with the rows split over the warps, the
-    // prefix read once per 64 of them.
+    // Up to 16 query rows per KV head in all: prefix_stream_kernel, whose warps split the keys.  More, and the head dim
+    // fits prefix_tc_kernel's tensor memory: that one.  d = 256: prefix_rows64_kernel, the prefix read once per 64 rows.
     pl->tc = !f32 && Bn * R > 16 && d <= 128;
     pl->rows_pre = f32 || Bn * R <= 16 ? 16 : 64;
     pl->rows_suf = 16;
@@ -575,14 +795,45 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
 }
 
 template <auto KERN>
-cudaError_t launch_attn(int smem, const PrefixParams& p, int rows, cudaStream_t st) {
+cudaError_t launch_items(int smem, const PrefixParams& p, int rows, cudaStream_t st) {
     const cudaError_t e = allow_smem<KERN>(smem);
     if (e != cudaSuccess) return e;
-    const long long n = (p.do_prefix ? (long long)cdiv(p.B * p.R, rows) * p.h_kv * p.n_pre : 0) +
-                        (p.do_suffix ? (long long)p.B * p.h_kv * cdiv(p.R, rows) * p.n_suf : 0);
+    const long long n = count_work(p, rows);
     if (n == 0) return cudaSuccess;
     if (n >= (1ll << 31)) return cudaErrorInvalidValue;
     KERN<<<(unsigned)n, 128, smem, st>>>(p);
+    return cudaPeekAtLastError();
+}
+
+// A K or V cache as boxes of 64 values x box_rows tokens: [slabs][rows][D].
+template <int D>
+bool cache_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t slabs, int box_rows) {
+    const uint64_t dims[3] = {(uint64_t)D, rows, slabs}, strides[2] = {D * 2ull, rows * D * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+    return make_tmap_nd(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box);
+}
+
+template <int D>
+cudaError_t launch_stream(const PrefixParams& p, cudaStream_t st) {
+    using C = StreamCfg<D>;
+    const long long n = count_work(p, C::ROWS);
+    if (n == 0) return cudaSuccess;
+    if (n >= (1ll << 30)) return cudaErrorInvalidValue;
+    CUtensorMap kp, vp, k, v;
+    const int box_rows = p.table ? std::min(C::TK, p.page_size) : C::TK;
+    const uint64_t rows = p.table ? p.page_size : p.Lmax, slabs = (uint64_t)(p.table ? p.num_pages : p.B) * p.h_kv;
+    bool ok = cache_map<D>(&k, p.k, rows, slabs, box_rows) && cache_map<D>(&v, p.v, rows, slabs, box_rows);
+    if (p.table || p.Lp == 0) {
+        kp = k;
+        vp = v;
+    } else {
+        ok = ok && cache_map<D>(&kp, p.kp, p.Lp, p.h_kv, box_rows) && cache_map<D>(&vp, p.vp, p.Lp, p.h_kv, box_rows);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const cudaError_t e = allow_smem<prefix_stream_kernel<D>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    const int blocks = (int)std::min<long long>(n, (long long)sm_count() * C::BLOCKS);
+    prefix_stream_kernel<D><<<blocks, 160, C::SMEM, st>>>(kp, vp, k, v, p, (int)n, box_rows);
     return cudaPeekAtLastError();
 }
 
@@ -596,13 +847,13 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
         if constexpr (D == 256) {
             TimedLaunch timer(st);
             p.do_suffix = 0;
-            e = launch_attn<prefix_mma_kernel<D, true>>(MmaCfg<D, true>::SMEM, p, 64, st);
+            e = launch_items<prefix_rows64_kernel<D>>(Rows64Cfg<D>::SMEM, p, 64, st);
             p.do_suffix = 1;
             p.do_prefix = 0;
             timer.stop();
         }
     }
-    if (e == cudaSuccess) e = launch_attn<prefix_mma_kernel<D, false>>(MmaCfg<D, false>::SMEM, p, 16, st);
+    if (e == cudaSuccess) e = launch_stream<D>(p, st);
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
     prefix_merge_kernel<__nv_bfloat16, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
@@ -612,7 +863,7 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
 template <int D>
 cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
     TimedLaunch timer(st);
-    const cudaError_t e = launch_attn<prefix_f32_kernel<D>>(F32Cfg<D>::SMEM, p, 16, st);
+    const cudaError_t e = launch_items<prefix_f32_kernel<D>>(F32Cfg<D>::SMEM, p, 16, st);
     timer.stop();
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
