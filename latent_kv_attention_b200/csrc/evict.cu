@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "launch_util.h"
 #include "mma.cuh"
 
 namespace lka {
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     __shared__ uint32_t s_prefix;
     __shared__ int s_need;
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    pdl_trigger();
     const int L = evict_len(p, b, tid == 0 && h == 0);
     const int n_out = min(L, p.budget);
     if (h == 0 && tid == 0) p.new_lens[b] = n_out;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int per = cdiv(n, m.ranges), r0 = min(n, range * per), r1 = min(n, r0 + per);
     const int32_t* kept = p.kept + ((size_t)b * p.h_kv + h) * p.budget;
     const int64_t bh = (int64_t)b * p.h_kv + h;
+    pdl_wait();
     if (what == 2 * m.slices) {  // the weights; the places behind the kept keys start from nothing
         move_rows<float>(p, reinterpret_cast<const uint8_t*>(p.w), reinterpret_cast<uint8_t*>(p.wo), bh * p.Lmax,
                          bh * p.Lout, nullptr, 4, 0, 1, kept, r0, r1);
@@ -283,9 +286,9 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     m.slices = cdiv(p.row_bytes, m.slice);
     const dim3 grid((2 * m.slices + 1) * m.ranges, p.h_kv, p.B);
     TimedLaunch timer(st);
-    evict_move_kernel<<<grid, kMoveThreads, 0, st>>>(p, m);
+    const cudaError_t e = launch_pdl<evict_move_kernel>(grid, kMoveThreads, 0, st, p, m);
     timer.stop();
-    return cudaPeekAtLastError() == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+    return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
 }
 
 }  // namespace

@@ -21,4 +21,27 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
+// Launches the next kernel of one call so that its blocks may start while the kernel before it still runs, from the
+// moment all blocks of that one have called pdl_trigger().  Whatever it needs of that kernel it takes after
+// pdl_wait(), which returns when the kernel has ended and its writes are visible.
+template <auto KERN, class... Args>
+cudaError_t launch_pdl(dim3 grid, int block, int smem, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, KERN, args...);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 }  // namespace lka

@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
         fence_barrier_init();
     }
     __syncthreads();
+    pdl_trigger();
 
     if (warp == 4) {
         // ------------------------------ producer: one lane per box of a tile ------------------------------
@@ -461,6 +462,8 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
         named_barrier(1, 128);  // the buffers are free for the next item
         if (!ok) s_abort = 1;
     }
+    // the merge waits for this kernel alone: it ends only after the prefix kernel before it
+    if (threadIdx.x == 0) pdl_wait();
 }
 
 // Many rows at d = 256 (whose accumulators do not fit prefix_tc_kernel's tensor memory twice): 64 query rows, 16 per
@@ -486,6 +489,7 @@ __global__ void __launch_bounds__(128) prefix_rows64_kernel(const PrefixParams p
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     Work w;
+    pdl_trigger();
     if (!find_work(p, C::ROWS, blockIdx.x, w, tid == 0)) return;
     const CacheRows rows = rows_of(p, w);
     const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(w.prefix ? p.kp : p.k);
@@ -571,6 +575,7 @@ __global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
     float* ps = vs + C::TK * D;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     Work w;
+    pdl_trigger();
     if (!find_work(p, C::ROWS, blockIdx.x, w, tid == 0)) return;
     const CacheRows rows = rows_of(p, w);
     const float* kb = static_cast<const float*>(w.prefix ? p.kp : p.k);
@@ -681,6 +686,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
     const int L = clamp_len(p.lens, b, p.Lmax, p.s, p.causal, p.status, false);
     const int seen = p.causal ? L - p.s + t + 1 : L;
     const int np = cdiv(P, p.pre_tokens), n = np + cdiv(seen, p.suf_tokens), gap = p.n_pre - np;
+    pdl_wait();
     const float* pl = p.part_lse + row * p.n_slots;
     float x[kMaxSlots / 32], M = -INFINITY;
 #pragma unroll
@@ -759,6 +765,23 @@ int split_keys(double units, double slots, int L, int tile, bool ragged = true) 
     return cdiv(lt, best) * tile;
 }
 
+// The same for persistent blocks, which run on from item to item: the work of a block (half a tile per item for its
+// start and join) and half an item's length as the tail.
+int stream_keys(double units, double slots, int L, int tile) {
+    const int lt = cdiv(std::max(L, 1), tile);
+    int best = 1;
+    double best_cost = -1.0;
+    for (int n = 1; n <= lt && n <= kMaxSplits; ++n) {
+        const int t = cdiv(lt, n);
+        const double cost = fmax(units * n / slots, 1.0) * (t + 0.5) + 0.5 * t;
+        if (best_cost < 0.0 || cost < best_cost - 1e-9) {
+            best_cost = cost;
+            best = n;
+        }
+    }
+    return cdiv(lt, best) * tile;
+}
+
 lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lmax, lka_dtype_t dtype, PrefixPlan* pl) {
     if (B < 0 || h_q < 1 || h_kv < 1 || s < 1 || d < 1 || Lp < 0 || Lmax < 1 || h_q % h_kv) return LKA_ERR_INVALID_ARG;
     if (dtype != LKA_BF16 && dtype != LKA_FP32) return LKA_ERR_UNSUPPORTED;
@@ -772,7 +795,8 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     pl->rows_pre = f32 || Bn * R <= 16 ? 16 : 64;
     pl->rows_suf = 16;
     const int tile = f32 ? 32 : 64;
-    const double slots = (double)sm_count() * (f32 ? 3 : d == 256 ? 1 : 2);
+    const double slots = (double)sm_count() * (f32 ? 3 : d == 256 ? 1 : d == 128 ? 2 : 3);
+    const bool rows64 = !f32 && !pl->tc && Bn * R > 16;
     // the split knob, where it leaves at most kMaxSplits splits
     const int knob = split_tokens_knob();
     auto by_knob = [knob](int L, int unit) { return cdiv(std::max(knob, cdiv(L, kMaxSplits)), unit) * unit; };
@@ -781,9 +805,11 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
                                   : split_keys((double)h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), sm_count(), Lp, 128, false);
     else
         pl->pre_tokens = knob > 0 ? by_knob(Lp, tile)
-                                  : split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile);
+                                  : f32 || rows64 ? split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile)
+                                                  : stream_keys((double)h_kv, slots, Lp, tile);
     pl->suf_tokens = knob > 0 ? by_knob(Lmax, tile)
-                              : split_keys((double)h_kv * Bn * cdiv(R, pl->rows_suf), slots, Lmax, tile);
+                              : f32 ? split_keys((double)h_kv * Bn * cdiv(R, pl->rows_suf), slots, Lmax, tile)
+                                    : stream_keys((double)h_kv * Bn * cdiv(R, pl->rows_suf), slots, Lmax, tile);
     pl->n_pre = cdiv(Lp, pl->pre_tokens);
     pl->n_suf = cdiv(Lmax, pl->suf_tokens);
     WsCarve c;
@@ -833,15 +859,20 @@ cudaError_t launch_stream(const PrefixParams& p, cudaStream_t st) {
     const cudaError_t e = allow_smem<prefix_stream_kernel<D>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const int blocks = (int)std::min<long long>(n, (long long)sm_count() * C::BLOCKS);
-    prefix_stream_kernel<D><<<blocks, 160, C::SMEM, st>>>(kp, vp, k, v, p, (int)n, box_rows);
-    return cudaPeekAtLastError();
+    if (p.do_prefix) {  // the call's first kernel
+        prefix_stream_kernel<D><<<blocks, 160, C::SMEM, st>>>(kp, vp, k, v, p, (int)n, box_rows);
+        return cudaPeekAtLastError();
+    }
+    return launch_pdl<prefix_stream_kernel<D>>(dim3(blocks), 160, C::SMEM, st, kp, vp, k, v, p, (int)n, box_rows);
 }
 
 template <int D>
 cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (pl.tc) {
-        if (p.n_pre > 0 && prefix_tc(p, D, st) != LKA_OK) return cudaErrorLaunchFailure;
+    if (p.n_pre == 0) {
+        // no prefix: the suffix kernel is the first
+    } else if (pl.tc) {
+        if (prefix_tc(p, D, st) != LKA_OK) return cudaErrorLaunchFailure;
         p.do_prefix = 0;
     } else if (pl.rows_pre > 16) {
         if constexpr (D == 256) {
@@ -856,8 +887,7 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_stream<D>(p, st);
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
-    prefix_merge_kernel<__nv_bfloat16, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
-    return cudaPeekAtLastError();
+    return launch_pdl<prefix_merge_kernel<__nv_bfloat16, D>>(dim3((unsigned)((rows + 3) / 4)), 128, 0, st, p);
 }
 
 template <int D>
@@ -867,8 +897,7 @@ cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
     timer.stop();
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)p.B * p.h_q * p.s;
-    prefix_merge_kernel<float, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
-    return cudaPeekAtLastError();
+    return launch_pdl<prefix_merge_kernel<float, D>>(dim3((unsigned)((rows + 3) / 4)), 128, 0, st, p);
 }
 
 lka_status_t prefix_run(PrefixParams& p, int d, float scale, lka_dtype_t dtype, void* ws, size_t ws_bytes,

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     const int n_qt = min(2, g.n_tiles - 2 * pair);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int P = prefix_length(p, threadIdx.x == 0 && blockIdx.x == 0);
+    pdl_trigger();  // the suffix kernel needs nothing of this one
     const int kbeg = split * p.pre_tokens, kend = min(P, kbeg + p.pre_tokens);
     if (kend <= kbeg) return;
     const int n_kt = cdiv(kend - kbeg, TK), nb = cdiv(kend - kbeg, TB);  // tiles of keys, blocks of scores
