@@ -176,7 +176,7 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
     pos = _dense(positions, "positions", torch.int32, dev, (B, s))
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out is x or (out.data_ptr() == x.data_ptr() and out.stride() == xs):
         _strided(out, "out", x.dtype, dev)
         _require(out.shape == shape, "out must have x's shape")
@@ -204,7 +204,7 @@ def _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out):
     if k.shape != (B, h_kv, s, d) or v.shape != k.shape:
         raise ValueError("q [B,h_q,s,d], k and v [B,h_kv,s,d]")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dt, device=dev)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(q_out, "q_out", dt, dev, shape)
     freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
@@ -280,7 +280,7 @@ def _latent_operands(q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out):
     freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
     _require(2 * inv_freq.numel() == d_r, "inv_freq must hold d_r / 2 values")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dt, device=dev)
+        q_out = torch.empty_like(q_r, memory_format=torch.contiguous_format)
     else:
         _dense(q_out, "q_out", dt, dev, shape)
     return (dev, code, B, h_q, s, c_kv.shape[3], d_r, q_out, _lens(cache_lens, B, dev),
@@ -336,7 +336,7 @@ def latent_rope_append_fp8kv(q_r, c_kv, k_r, latent, kv_scale, cache_lens, inv_f
 def _attn_outputs(q, out, return_lse):
     B, h_q, s, d = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     else:
         _dense(out, "out", q.dtype, q.device, q.shape)
     lse = torch.empty((B, h_q, s), dtype=torch.float32, device=q.device) if return_lse else None
@@ -444,9 +444,8 @@ def gqa_key_weights_paged(q, k_pages, lse, block_table, cache_lens, weights=None
     return weights
 
 
-def _evict_outputs(B, h_kv, budget, dev):
-    return (torch.empty((B,), dtype=torch.int32, device=dev),
-            torch.empty((B, h_kv, budget), dtype=torch.int32, device=dev))
+def _evict_outputs(cache_lens, h_kv, budget):
+    return torch.empty_like(cache_lens), cache_lens.new_empty((cache_lens.shape[0], h_kv, budget))
 
 
 def gqa_evict(k, v, weights, cache_lens, budget: int, sinks: int = 0, recent: int = 0, k_out=None, v_out=None,
@@ -475,9 +474,9 @@ def gqa_evict(k, v, weights, cache_lens, budget: int, sinks: int = 0, recent: in
     _require(to[2] >= budget, "k_out holds fewer rows than the budget")
     if weights_out is None:
         _require(ko != kp or k.numel() == 0, "in place needs weights_out=weights")
-        weights_out = torch.empty(to[:3], dtype=torch.float32, device=dev)
+        weights_out = weights.new_empty(to[:3])
     wo = _dense(weights_out, "weights_out", torch.float32, dev, to[:3])
-    new_lens, kept = _evict_outputs(B, h_kv, budget, dev)
+    new_lens, kept = _evict_outputs(cache_lens, h_kv, budget)
     _call("gqa_evict", dev, (kp, vp, wp, lens, ko, vo, wo, new_lens.data_ptr(), kept.data_ptr(), B, h_kv, d, Lmax, to[2],
                              budget, sinks, recent, _CACHE_DT[dt]))
     return k_out, v_out, weights_out, new_lens, kept
@@ -501,7 +500,7 @@ def gqa_evict_paged(k_pages, v_pages, weights, block_table, cache_lens, budget: 
     budget, sinks, recent = int(budget), int(sinks), int(recent)
     _require(1 <= budget <= max_pages * page_size and sinks >= 0 and recent >= 0,
              "budget must be between 1 and the table's capacity, sinks and recent at least 0")
-    new_lens, kept = _evict_outputs(B, h_kv, budget, dev)
+    new_lens, kept = _evict_outputs(cache_lens, h_kv, budget)
     _call("gqa_evict_paged", dev, (kp, vp, wp, table, lens, new_lens.data_ptr(), kept.data_ptr(), B, h_kv, d, page_size,
                                    max_pages, num_pages, budget, sinks, recent, _CACHE_DT[dt]))
     return new_lens, kept

@@ -13,12 +13,15 @@
 // [-1/2, 1/2] there, and only the reduced turn goes to fp32 (sincospi): two fp64
 // operations per (token, pair), shared by every head of the token.
 //
-// Bound: HBM (about 0.75 operations per byte moved), or launch latency for a
-// decode step.  One CTA takes one token (its cos / sin table is made once, in
-// shared memory, for all heads); each thread moves units of two 16-byte vectors
-// (the two halves of VE pairs, or 2 VE pairs side by side), issues the loads of up
-// to four units before it computes, and rounds once, on the way out.  While there
-// are few tokens, the units of one token are spread over several CTAs instead.
+// Bound: HBM (about 0.75 operations per byte moved), or launch latency for a decode step.
+// A CTA takes a few consecutive tokens: their cos / sin tables are made once, in shared
+// memory, for all heads; then every thread keeps to one unit of a head -- VE pairs, two
+// 16-byte vectors -- and walks (token, head) over queries, keys and values (one row of
+// "virtual heads"), four units in flight, rounding once, on the way out.  The first loads are
+// issued before the tables are made.  With one token per CTA the chain length, position, angle,
+// table, barrier came once per 8 to 12 KB and bound (4096 x 4 tokens of 32 heads of 128,
+// backward: 43 us; several tokens per CTA: see below).  While there are few tokens, the heads
+// of one token are spread over several CTAs instead.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -48,14 +51,18 @@ struct RopeParams {
     int B, s, h_q, h_kv, d, dv, n, Lmax, page_size, max_pages, num_pages;
     float amplitude;
     float sign;  // +1, or -1 for the backward pass
-    int units, units_per_cta;
+    int width;          // units a head is walked in: the block is `lanes` heads x width units
+    int lanes, vheads, vsub;  // virtual heads in all, and per value head
+    int heads_per_cta;
+    int tokens_per_cta;       // 1 where the heads are spread over several CTAs
 };
 
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeBatch = 4;     // units in flight per thread
+constexpr int kRopeBatch = 4;  // units in flight per thread
 constexpr int kRopeMaxPairs = 256;
+constexpr int kRopeMaxTokens = 8, kRopeTable = 512;  // tokens per CTA, (cos, sin) pairs of its tables
 
 template <typename T, int VE>
 struct VecOf;
@@ -75,25 +82,47 @@ __device__ __forceinline__ void unpack(const typename VecOf<T, VE>::V& u, float*
     for (int i = 0; i < VE; ++i) f[i] = to_f32<T>(e[i]);
 }
 
-// VE values to the destination type, in one store.  e4m3: value / scale, rounded to nearest even, saturated.
+// VE values to the destination type, in one store.
 template <typename C, int VE>
-__device__ __forceinline__ void store_vec(void* base, long long at, const float* f, float scale) {
-    if constexpr (sizeof(C) == 1) {
-        uint8_t b[VE];
+__device__ __forceinline__ void store_vec(void* base, int64_t at, const float* f) {
+    typename VecOf<C, VE>::V u;
+    C* e = reinterpret_cast<C*>(&u);
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-            b[i] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(f[i], scale), __NV_SATFINITE, __NV_E4M3);
-        uint8_t* p = static_cast<uint8_t*>(base) + at;
+    for (int i = 0; i < VE; ++i) e[i] = from_f32<C>(f[i]);
+    *reinterpret_cast<typename VecOf<C, VE>::V*>(static_cast<C*>(base) + at) = u;
+}
+
+// A per-head scale of an e4m3 cache and how to divide by it.  For scales of ordinary size x / s is the product with the
+// rounded reciprocal r and one correction, q + (x - q s) r: the correctly rounded quotient (Markstein's theorem) in
+// three operations; for others, and for infinite quotients, the division itself.
+struct Scale {
+    float s, r;
+    bool plain;
+};
+__device__ __forceinline__ Scale make_scale(float s) {
+    return {s, __frcp_rn(s), fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f};
+}
+__device__ __forceinline__ float quotient(float x, const Scale& c) {
+    if (!c.plain) return __fdiv_rn(x, c.s);
+    const float q = __fmul_rn(x, c.r), e = __fmaf_rn(-q, c.s, x);
+    return fabsf(q) < 0x1p100f ? __fmaf_rn(e, c.r, q) : q;
+}
+// VE values as e4m3 of value / scale, rounded to nearest even and saturated.
+template <int VE>
+__device__ __forceinline__ void store_e4m3(void* base, int64_t at, const float* f, const Scale& c) {
+    uint8_t* p = static_cast<uint8_t*>(base) + at;
+    if constexpr (VE == 1) {
+        *p = (uint8_t)__nv_cvt_float_to_fp8(quotient(f[0], c), __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint16_t b[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE; i += 2)
+            b[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(f[i], c), quotient(f[i + 1], c)), __NV_SATFINITE,
+                                                __NV_E4M3);
         if constexpr (VE == 8)
             *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(b);
         else
-            p[0] = b[0];
-    } else {
-        typename VecOf<C, VE>::V u;
-        C* e = reinterpret_cast<C*>(&u);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) e[i] = from_f32<C>(f[i]);
-        *reinterpret_cast<typename VecOf<C, VE>::V*>(static_cast<C*>(base) + at) = u;
+            *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<uint32_t*>(b);
     }
 }
 
@@ -101,148 +130,190 @@ __device__ __forceinline__ void store_vec(void* base, long long at, const float*
 __host__ __device__ inline int rot_units(int n, int ve) { return (n + ve - 1) / ve; }
 __host__ __device__ inline int copy_units(int values, int ve) { return (values + 2 * ve - 1) / (2 * ve); }
 
+// Where a token's data lies, in elements.
+struct RopeToken {
+    int64_t q, k, v, out, cache;
+    double pos;
+    int live, store;  // a padding token is not live: zeros for its queries; store: its cache row is written
+};
+
 // T: element of q, k, v and q_out; C: element of the cache; VE: values per vector (1: no alignment needed).
 template <typename T, typename C, int VE, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
     using V = typename VecOf<T, VE>::V;
-    __shared__ float2 cs[kRopeMaxPairs];
-    const int tok = blockIdx.x, b = tok / p.s, t = tok % p.s;
-
-    // the token's cache row (-1: a padding token, or one whose place is not in the cache)
-    int row = t, slab = b;
-    bool live = true;
-    if (p.lens) {
-        const int L = p.lens[b];
-        const bool bad = L < 0 || L > p.Lmax;
-        if (bad && t == 0 && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, kDevBadLength);
-        row = L - p.s + t;
-        live = !bad && row >= 0;
-    }
-    bool store = live;
-    int in_slab = row;
-    if (p.table && live) {
-        const int page = p.table[(size_t)b * p.max_pages + row / p.page_size];
-        if (page < 0 || page >= p.num_pages) {
-            if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, kDevBadPage);
-            store = false;
+    __shared__ float2 cs[kRopeTable];
+    __shared__ RopeToken tokens[kRopeMaxTokens];
+    const int tok0 = blockIdx.x * p.tokens_per_cta, n_tok = min(p.tokens_per_cta, p.B * p.s - tok0);
+    if (threadIdx.x < n_tok) {
+        const int tok = tok0 + threadIdx.x, b = tok / p.s, t = tok % p.s;
+        int row = t, slab = b;
+        bool live = true;
+        if (p.lens) {
+            const int L = p.lens[b];
+            const bool bad = L < 0 || L > p.Lmax;
+            if (bad && t == 0 && blockIdx.y == 0) atomicOr(p.status, kDevBadLength);
+            row = L - p.s + t;
+            live = !bad && row >= 0;
         }
-        slab = page;
-        in_slab = row % p.page_size;
+        bool store = live;
+        int in_slab = row;
+        if (p.table && live) {
+            const int page = p.table[(size_t)b * p.max_pages + row / p.page_size];
+            if (page < 0 || page >= p.num_pages) {
+                if (blockIdx.y == 0) atomicOr(p.status, kDevBadPage);
+                store = false;
+            }
+            slab = page;
+            in_slab = row % p.page_size;
+        }
+        RopeToken o;
+        o.q = b * p.qs.b + t * p.qs.s;
+        o.k = b * p.ks.b + t * p.ks.s;
+        o.v = b * p.vs.b + t * p.vs.s;
+        o.out = b * p.os.b + t * p.os.s;
+        o.cache = slab * p.slab + in_slab * p.row;
+        o.pos = p.positions ? (double)p.positions[tok] : (double)row;
+        o.live = live;
+        o.store = store;
+        tokens[threadIdx.x] = o;
     }
+    __syncthreads();
 
-    const int nrot = rot_units(p.n, VE), upq = nrot + copy_units(p.d - 2 * p.n, VE);
-    const int upv = p.v ? copy_units(p.dv, VE) : 0;
-    const int uq = p.h_q * upq, uk = p.k ? p.h_kv * upq : 0;
-    const int u_end = min(p.units, ((int)blockIdx.y + 1) * p.units_per_cta);
+    const int nrot = rot_units(p.n, VE), upq = nrot + copy_units(p.d - 2 * p.n, VE), upv = copy_units(p.dv, VE);
+    const int unit0 = threadIdx.x % p.width, lane_h = threadIdx.x / p.width;
+    const int first_k = p.h_q, first_v = p.h_q + p.h_kv;
+    const int h0 = blockIdx.y * p.heads_per_cta, h_end = min(p.vheads, h0 + p.heads_per_cta);
+    const int per_tok = cdiv(h_end - h0, p.lanes), items = per_tok * n_tok;  // (token, head of this thread) pairs
     bool have_table = false;
 
-    for (int u0 = blockIdx.y * p.units_per_cta; u0 < u_end; u0 += kRopeThreads * kRopeBatch) {
-        V x[kRopeBatch][2];
+    // one pass unless a head has more units than the block has threads
+    for (int w = unit0; w - unit0 < upq; w += p.width) {
+        const bool turn = w < nrot, on = lane_h < p.lanes && w < upq;
+        // columns of the unit's two vectors in a q or k head
+        const int c0 = turn ? (INTER ? 2 * VE * w : VE * w) : 2 * p.n + 2 * VE * (w - nrot);
+        const int c1 = turn && !INTER ? c0 + p.n : c0 + VE;
+        for (int i0 = 0; i0 < items; i0 += kRopeBatch) {
+            V x[kRopeBatch][2];
+            int tt = i0 / per_tok, hk = i0 - tt * per_tok;
+            const int tt0 = tt, hk0 = hk;
 #pragma unroll
-        for (int j = 0; j < kRopeBatch; ++j) {
-            const int u = u0 + j * kRopeThreads + threadIdx.x;
-            x[j][0] = V{};
-            x[j][1] = V{};
-            if (u >= u_end || !live) continue;
-            const T* src;
-            int w, c0, c1, width = p.d;  // unit in the head, columns of its two vectors
-            if (u < uq) {
-                const int h = u / upq;
-                w = u - h * upq;
-                src = static_cast<const T*>(p.q) + b * p.qs.b + h * p.qs.h + t * p.qs.s;
-            } else if (u < uq + uk) {
-                const int h = (u - uq) / upq;
-                w = u - uq - h * upq;
-                src = static_cast<const T*>(p.k) + b * p.ks.b + h * p.ks.h + t * p.ks.s;
-            } else {
-                const int h = (u - uq - uk) / upv;
-                w = u - uq - uk - h * upv + nrot;
-                src = static_cast<const T*>(p.v) + b * p.vs.b + h * p.vs.h + t * p.vs.s;
-                width = p.dv;
+            for (int j = 0; j < kRopeBatch; ++j) {
+                const int h = h0 + hk * p.lanes + lane_h;
+                x[j][0] = V{};
+                x[j][1] = V{};
+                if (on && tt < n_tok && h < h_end && tokens[tt].live) {
+                    if (h < first_v) {
+                        const T* src = h < first_k ? static_cast<const T*>(p.q) + tokens[tt].q + h * p.qs.h
+                                                   : static_cast<const T*>(p.k) + tokens[tt].k + (h - first_k) * p.ks.h;
+                        x[j][0] = *reinterpret_cast<const V*>(src + c0);
+                        if (c1 < p.d) x[j][1] = *reinterpret_cast<const V*>(src + c1);
+                    } else {
+                        const int hv = (h - first_v) / p.vsub, wv = (h - first_v) % p.vsub * upq + w;
+                        const T* src = static_cast<const T*>(p.v) + tokens[tt].v + hv * p.vs.h + 2 * VE * wv;
+                        if (wv < upv) {
+                            x[j][0] = *reinterpret_cast<const V*>(src);
+                            if (2 * VE * wv + VE < p.dv) x[j][1] = *reinterpret_cast<const V*>(src + VE);
+                        }
+                    }
+                }
+                if (++hk == per_tok) {
+                    hk = 0;
+                    ++tt;
+                }
             }
-            if (w < nrot) {
-                c0 = INTER ? 2 * VE * w : VE * w;
-                c1 = INTER ? c0 + VE : c0 + p.n;
-            } else {
-                c0 = (u < uq + uk ? 2 * p.n : 0) + 2 * VE * (w - nrot);
-                c1 = c0 + VE;
-            }
-            x[j][0] = *reinterpret_cast<const V*>(src + c0);
-            if (c1 < width) x[j][1] = *reinterpret_cast<const V*>(src + c1);
-        }
-        if (!have_table) {
-            if (live) {
-                const double pos = p.positions ? (double)p.positions[(size_t)b * p.s + t] : (double)row;
-                for (int i = threadIdx.x; i < p.n; i += kRopeThreads) {
-                    const double turn = pos * (p.inv_freq[i] * 0.15915494309189533577);
+            if (!have_table) {
+                for (int i = threadIdx.x; i < n_tok * p.n; i += kRopeThreads) {
+                    const int k = i / p.n;
+                    const double turns = tokens[k].pos * (p.inv_freq[i - k * p.n] * 0.15915494309189533577);
                     float sn, cn;
-                    sincospif(2.0f * (float)(turn - rint(turn)), &sn, &cn);
+                    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
                     cs[i] = make_float2(cn * p.amplitude, sn * p.amplitude * p.sign);
                 }
+                __syncthreads();
+                have_table = true;
             }
-            __syncthreads();
-            have_table = true;
-        }
+            tt = tt0;
+            hk = hk0;
 #pragma unroll
-        for (int j = 0; j < kRopeBatch; ++j) {
-            const int u = u0 + j * kRopeThreads + threadIdx.x;
-            if (u >= u_end) continue;
-            float a[VE], c[VE];
-            unpack<T, VE>(x[j][0], a);
-            unpack<T, VE>(x[j][1], c);
-            const bool is_q = u < uq, is_v = u >= uq + uk;
-            const int per = is_v ? upv : upq, first = is_q ? 0 : is_v ? uq + uk : uq;
-            const int h = (u - first) / per, w = u - first - h * per;
-            const bool turn = !is_v && w < nrot;
-            int c0, c1;
-            if (turn) {
-                c0 = INTER ? 2 * VE * w : VE * w;
-                c1 = INTER ? c0 + VE : c0 + p.n;
-                if constexpr (INTER) {
-                    // pairs lie side by side in the 2 VE values
-                    float z[2 * VE];
+            for (int j = 0; j < kRopeBatch; ++j) {
+                const int h = h0 + hk * p.lanes + lane_h, at = tt;
+                if (++hk == per_tok) {
+                    hk = 0;
+                    ++tt;
+                }
+                if (!on || at >= n_tok || h >= h_end) continue;
+                const bool store = tokens[at].store;
+                if (h < first_v) {
+                    if (h >= first_k && !store) continue;
+                    float a[VE], c[VE];
+                    unpack<T, VE>(x[j][0], a);
+                    unpack<T, VE>(x[j][1], c);
+                    if (turn) {
+                        const float2* r = cs + at * p.n + VE * w;
+                        if constexpr (INTER) {
+                            // pairs lie side by side in the 2 VE values
+                            float z[2 * VE];
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        z[i] = a[i];
-                        z[VE + i] = c[i];
+                            for (int i = 0; i < VE; ++i) {
+                                z[i] = a[i];
+                                z[VE + i] = c[i];
+                            }
+#pragma unroll
+                            for (int i = 0; i < VE; ++i) {
+                                const float x0 = z[2 * i], x1 = z[2 * i + 1];
+                                z[2 * i] = x0 * r[i].x - x1 * r[i].y;
+                                z[2 * i + 1] = x1 * r[i].x + x0 * r[i].y;
+                            }
+#pragma unroll
+                            for (int i = 0; i < VE; ++i) {
+                                a[i] = z[i];
+                                c[i] = z[VE + i];
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < VE; ++i) {
+                                const float x0 = a[i], x1 = c[i];
+                                a[i] = x0 * r[i].x - x1 * r[i].y;
+                                c[i] = x1 * r[i].x + x0 * r[i].y;
+                            }
+                        }
                     }
+                    if (h < first_k) {
+                        if (!tokens[at].live) {  // zeros, whatever the table holds for the missing position
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        const float2 r = live ? cs[VE * w + i] : make_float2(0.f, 0.f);
-                        const float x0 = z[2 * i], x1 = z[2 * i + 1];
-                        z[2 * i] = x0 * r.x - x1 * r.y;
-                        z[2 * i + 1] = x1 * r.x + x0 * r.y;
+                            for (int i = 0; i < VE; ++i) a[i] = c[i] = 0.f;
+                        }
+                        const int64_t o = tokens[at].out + h * p.os.h;
+                        store_vec<T, VE>(p.q_out, o + c0, a);
+                        if (c1 < p.d) store_vec<T, VE>(p.q_out, o + c1, c);
+                    } else {
+                        const int64_t o = tokens[at].cache + (h - first_k) * p.k_head;
+                        if constexpr (sizeof(C) == 1) {
+                            const Scale sc = make_scale(p.k_scale[p.scale_by_head ? h - first_k : 0]);
+                            store_e4m3<VE>(p.kc, o + c0, a, sc);
+                            if (c1 < p.d) store_e4m3<VE>(p.kc, o + c1, c, sc);
+                        } else {
+                            store_vec<C, VE>(p.kc, o + c0, a);
+                            if (c1 < p.d) store_vec<C, VE>(p.kc, o + c1, c);
+                        }
                     }
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        a[i] = z[i];
-                        c[i] = z[VE + i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        const float2 r = live ? cs[VE * w + i] : make_float2(0.f, 0.f);
-                        const float x0 = a[i], x1 = c[i];
-                        a[i] = x0 * r.x - x1 * r.y;
-                        c[i] = x1 * r.x + x0 * r.y;
+                } else if (store) {
+                    const int hv = (h - first_v) / p.vsub, wv = (h - first_v) % p.vsub * upq + w;
+                    if (wv >= upv) continue;
+                    const bool two = 2 * VE * wv + VE < p.dv;
+                    const int64_t o = tokens[at].cache + hv * p.v_head + 2 * VE * wv;
+                    if constexpr (sizeof(C) == 1) {
+                        float a[VE], c[VE];
+                        unpack<T, VE>(x[j][0], a);
+                        unpack<T, VE>(x[j][1], c);
+                        const Scale sc = make_scale(p.v_scale[p.scale_by_head ? hv : 0]);
+                        store_e4m3<VE>(p.vc, o, a, sc);
+                        if (two) store_e4m3<VE>(p.vc, o + VE, c, sc);
+                    } else {  // the same type: the bits
+                        *reinterpret_cast<V*>(static_cast<C*>(p.vc) + o) = x[j][0];
+                        if (two) *reinterpret_cast<V*>(static_cast<C*>(p.vc) + o + VE) = x[j][1];
                     }
                 }
-            } else {
-                c0 = is_v ? 2 * VE * w : 2 * p.n + 2 * VE * (w - nrot);
-                c1 = c0 + VE;
-            }
-            const int width = is_v ? p.dv : p.d;
-            if (is_q) {
-                const long long o = b * p.os.b + h * p.os.h + t * p.os.s;
-                store_vec<T, VE>(p.q_out, o + c0, a, 1.f);
-                if (c1 < width) store_vec<T, VE>(p.q_out, o + c1, c, 1.f);
-            } else if (store) {
-                const float* sc = is_v ? p.v_scale : p.k_scale;
-                const float scale = sizeof(C) == 1 ? sc[p.scale_by_head ? h : 0] : 1.f;
-                void* base = is_v ? p.vc : p.kc;
-                const long long o = slab * p.slab + h * (is_v ? p.v_head : p.k_head) + in_slab * p.row;
-                store_vec<C, VE>(base, o + c0, a, scale);
-                if (c1 < width) store_vec<C, VE>(base, o + c1, c, scale);
             }
         }
     }
@@ -266,19 +337,25 @@ cudaError_t rope_launch(RopeParams& p, bool inter, cudaStream_t st) {
     }
     const int ve = vec ? W : 1;
     const int upq = rot_units(p.n, ve) + copy_units(p.d - 2 * p.n, ve);
-    const long long units = (long long)(p.h_q + (p.k ? p.h_kv : 0)) * upq +
-                            (p.v ? (long long)p.h_kv * copy_units(p.dv, ve) : 0);
-    if (units >= (1ll << 31)) return cudaErrorInvalidValue;
-    p.units = (int)units;
+    p.width = std::min(upq, kRopeThreads);
+    p.lanes = kRopeThreads / p.width;
+    p.vsub = p.v ? cdiv(copy_units(p.dv, ve), upq) : 0;
+    const long long vheads = p.h_q + (p.k ? (long long)p.h_kv * (1 + p.vsub) : 0);
+    if (vheads >= (1ll << 30)) return cudaErrorInvalidValue;
+    p.vheads = (int)vheads;
+    if (!p.k) p.h_kv = 0;
     const long long tokens = (long long)p.B * p.s;
-    // few tokens: one batch of loads per thread at most, spread over the SMs; many: one CTA per token
-    p.units_per_cta = p.units;
+    // Many tokens: several per CTA, as long as that leaves every SM a few CTAs and the tables fit; few: one head per
+    // thread, spread over the SMs.
+    p.heads_per_cta = p.vheads;
+    p.tokens_per_cta = (int)std::max(1LL, std::min({tokens / (8LL * sm_count()), (long long)kRopeMaxTokens,
+                                                    (long long)(kRopeTable / p.n)}));
     if (tokens < 4LL * sm_count()) {
         const int want = (int)((4LL * sm_count() + tokens - 1) / tokens);
-        p.units_per_cta = std::max(kRopeThreads, cdiv(p.units, want));
+        p.heads_per_cta = std::max(p.lanes, cdiv(cdiv(p.vheads, want), p.lanes) * p.lanes);
     }
-    p.units_per_cta = std::max(p.units_per_cta, cdiv(p.units, 32768));
-    const dim3 grid((unsigned)tokens, cdiv(p.units, p.units_per_cta));
+    p.heads_per_cta = std::max(p.heads_per_cta, cdiv(p.vheads, 32768));
+    const dim3 grid((unsigned)((tokens + p.tokens_per_cta - 1) / p.tokens_per_cta), cdiv(p.vheads, p.heads_per_cta));
     TimedLaunch timer(st);
     if (vec) {
         if (inter)
