@@ -59,7 +59,7 @@ struct RopeParams {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 128, kRopeBlocks = 7;  // per SM
 constexpr int kRopeBatch = 4;  // units in flight per thread
 constexpr int kRopeMaxPairs = 256;
 constexpr int kRopeMaxTokens = 8, kRopeTable = 512;  // tokens per CTA, (cos, sin) pairs of its tables
@@ -130,6 +130,13 @@ __device__ __forceinline__ void store_e4m3(void* base, int64_t at, const float* 
 __host__ __device__ inline int rot_units(int n, int ve) { return (n + ve - 1) / ve; }
 __host__ __device__ inline int copy_units(int values, int ve) { return (values + 2 * ve - 1) / (2 * ve); }
 
+// Place of pair i in a token's table of n: two pairs side by side, then the same two of the next unit, so that the
+// threads of consecutive units read consecutive 16 bytes (in the order of the pairs they would meet in the same banks).
+template <int VE>
+__device__ __forceinline__ int table_at(int i, int n) {
+    return VE == 1 ? i : ((i % VE / 2) * (n / VE) + i / VE) * 2 + (i & 1);
+}
+
 // Where a token's data lies, in elements.
 struct RopeToken {
     int64_t q, k, v, out, cache;
@@ -139,9 +146,9 @@ struct RopeToken {
 
 // T: element of q, k, v and q_out; C: element of the cache; VE: values per vector (1: no alignment needed).
 template <typename T, typename C, int VE, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeParams p) {
     using V = typename VecOf<T, VE>::V;
-    __shared__ float2 cs[kRopeTable];
+    __shared__ __align__(16) float2 cs[kRopeTable];
     __shared__ RopeToken tokens[kRopeMaxTokens];
     const int tok0 = blockIdx.x * p.tokens_per_cta, n_tok = min(p.tokens_per_cta, p.B * p.s - tok0);
     if (threadIdx.x < n_tok) {
@@ -227,7 +234,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                     const double turns = tokens[k].pos * (p.inv_freq[i - k * p.n] * 0.15915494309189533577);
                     float sn, cn;
                     sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
-                    cs[i] = make_float2(cn * p.amplitude, sn * p.amplitude * p.sign);
+                    cs[k * p.n + table_at<VE>(i - k * p.n, p.n)] =
+                        make_float2(cn * p.amplitude, sn * p.amplitude * p.sign);
                 }
                 __syncthreads();
                 have_table = true;
@@ -249,7 +257,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                     unpack<T, VE>(x[j][0], a);
                     unpack<T, VE>(x[j][1], c);
                     if (turn) {
-                        const float2* r = cs + at * p.n + VE * w;
+                        float2 r[VE];
+#pragma unroll
+                        for (int i = 0; i < VE; i += 2) {
+                            const float2* from = cs + at * p.n + table_at<VE>(VE * w + i, p.n);
+                            if constexpr (VE == 1) {
+                                r[0] = from[0];
+                            } else {
+                                const float4 two = *reinterpret_cast<const float4*>(from);
+                                r[i] = make_float2(two.x, two.y);
+                                r[i + 1] = make_float2(two.z, two.w);
+                            }
+                        }
                         if constexpr (INTER) {
                             // pairs lie side by side in the 2 VE values
                             float z[2 * VE];
@@ -345,11 +364,12 @@ cudaError_t rope_launch(RopeParams& p, bool inter, cudaStream_t st) {
     p.vheads = (int)vheads;
     if (!p.k) p.h_kv = 0;
     const long long tokens = (long long)p.B * p.s;
-    // Many tokens: several per CTA, as long as that leaves every SM a few CTAs and the tables fit; few: one head per
+    // Many tokens: several per CTA, as many as the tables hold, such that the CTAs fill whole waves; few: one head per
     // thread, spread over the SMs.
     p.heads_per_cta = p.vheads;
-    p.tokens_per_cta = (int)std::max(1LL, std::min({tokens / (8LL * sm_count()), (long long)kRopeMaxTokens,
-                                                    (long long)(kRopeTable / p.n)}));
+    const long long slots = (long long)kRopeBlocks * sm_count(), most = std::min(kRopeMaxTokens, kRopeTable / p.n);
+    const long long waves = (tokens + slots * most - 1) / (slots * most);
+    p.tokens_per_cta = (int)((tokens + slots * waves - 1) / (slots * waves));
     if (tokens < 4LL * sm_count()) {
         const int want = (int)((4LL * sm_count() + tokens - 1) / tokens);
         p.heads_per_cta = std::max(p.lanes, cdiv(cdiv(p.vheads, want), p.lanes) * p.lanes);
