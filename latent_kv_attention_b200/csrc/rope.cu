@@ -16,15 +16,14 @@
 // Bound: HBM (about 0.75 operations per byte moved), or launch latency for a decode step.
 // A CTA takes a few consecutive tokens: their cos / sin tables are made once, in shared
 // memory, for all heads; then every thread keeps to one unit of a head -- VE pairs, two
-// 16-byte vectors -- and walks (token, head) over queries, keys and values (one row of
-// "virtual heads"), four units in flight, rounding once, on the way out.  The first loads are
-// issued before the tables are made.  With one token per CTA the chain length, position, angle,
-// table, barrier came once per 8 to 12 KB and bound (4096 x 4 tokens of 32 heads of 128,
-// backward: 43 us; several tokens per CTA: see below).  While there are few tokens, the heads
-// of one token are spread over several CTAs instead.
+// 16-byte vectors -- and carries it through all tokens, four in flight, so that what depends
+// on the head (which tensor, addresses, scale) is worked out once per head and what depends on
+// the token comes from shared memory.  While there are few tokens, the heads of one token are
+// spread over several CTAs instead.
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -137,22 +136,24 @@ __device__ __forceinline__ int table_at(int i, int n) {
     return VE == 1 ? i : ((i % VE / 2) * (n / VE) + i / VE) * 2 + (i & 1);
 }
 
-// Where a token's data lies, in elements.
-struct RopeToken {
-    int64_t q, k, v, out, cache;
-    double pos;
-    int live, store;  // a padding token is not live: zeros for its queries; store: its cache row is written
+// Where the CTA's tokens lie, in elements.
+struct RopeTokens {
+    int64_t q[kRopeMaxTokens], k[kRopeMaxTokens], v[kRopeMaxTokens], out[kRopeMaxTokens], cache[kRopeMaxTokens];
+    double pos[kRopeMaxTokens];
+    int live[kRopeMaxTokens], store[kRopeMaxTokens];  // a padding token is not live: its queries are 0; store: its cache row is written
 };
+
+enum RopeKind { kRotateQuery, kRotateKey, kCopyValue };
 
 // T: element of q, k, v and q_out; C: element of the cache; VE: values per vector (1: no alignment needed).
 template <typename T, typename C, int VE, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeParams p) {
     using V = typename VecOf<T, VE>::V;
     __shared__ __align__(16) float2 cs[kRopeTable];
-    __shared__ RopeToken tokens[kRopeMaxTokens];
+    __shared__ RopeTokens at;
     const int tok0 = blockIdx.x * p.tokens_per_cta, n_tok = min(p.tokens_per_cta, p.B * p.s - tok0);
     if (threadIdx.x < n_tok) {
-        const int tok = tok0 + threadIdx.x, b = tok / p.s, t = tok % p.s;
+        const int i = threadIdx.x, tok = tok0 + i, b = tok / p.s, t = tok % p.s;
         int row = t, slab = b;
         bool live = true;
         if (p.lens) {
@@ -173,166 +174,139 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const R
             slab = page;
             in_slab = row % p.page_size;
         }
-        RopeToken o;
-        o.q = b * p.qs.b + t * p.qs.s;
-        o.k = b * p.ks.b + t * p.ks.s;
-        o.v = b * p.vs.b + t * p.vs.s;
-        o.out = b * p.os.b + t * p.os.s;
-        o.cache = slab * p.slab + in_slab * p.row;
-        o.pos = p.positions ? (double)p.positions[tok] : (double)row;
-        o.live = live;
-        o.store = store;
-        tokens[threadIdx.x] = o;
+        at.q[i] = b * p.qs.b + t * p.qs.s;
+        at.k[i] = b * p.ks.b + t * p.ks.s;
+        at.v[i] = b * p.vs.b + t * p.vs.s;
+        at.out[i] = b * p.os.b + t * p.os.s;
+        at.cache[i] = slab * p.slab + in_slab * p.row;
+        at.pos[i] = p.positions ? (double)p.positions[tok] : (double)row;
+        at.live[i] = live;
+        at.store[i] = store;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_tok * p.n; i += kRopeThreads) {
+        const int k = i / p.n;
+        const double turns = at.pos[k] * (p.inv_freq[i - k * p.n] * 0.15915494309189533577);
+        float sn, cn;
+        sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
+        cs[k * p.n + table_at<VE>(i - k * p.n, p.n)] = make_float2(cn * p.amplitude, sn * p.amplitude * p.sign);
     }
     __syncthreads();
 
     const int nrot = rot_units(p.n, VE), upq = nrot + copy_units(p.d - 2 * p.n, VE), upv = copy_units(p.dv, VE);
-    const int unit0 = threadIdx.x % p.width, lane_h = threadIdx.x / p.width;
+    const int lane_h = threadIdx.x / p.width;
+    if (lane_h >= p.lanes) return;
     const int first_k = p.h_q, first_v = p.h_q + p.h_kv;
     const int h0 = blockIdx.y * p.heads_per_cta, h_end = min(p.vheads, h0 + p.heads_per_cta);
-    const int per_tok = cdiv(h_end - h0, p.lanes), items = per_tok * n_tok;  // (token, head of this thread) pairs
-    bool have_table = false;
 
-    // one pass unless a head has more units than the block has threads
-    for (int w = unit0; w - unit0 < upq; w += p.width) {
-        const bool turn = w < nrot, on = lane_h < p.lanes && w < upq;
-        // columns of the unit's two vectors in a q or k head
-        const int c0 = turn ? (INTER ? 2 * VE * w : VE * w) : 2 * p.n + 2 * VE * (w - nrot);
-        const int c1 = turn && !INTER ? c0 + p.n : c0 + VE;
-        for (int i0 = 0; i0 < items; i0 += kRopeBatch) {
+    // One unit of one head over all tokens of the CTA: src + from[token] -> dst + to[token]; the unit's second vector
+    // lies `delta` after the first (two: it exists), in both.
+    auto walk = [&](auto kind_c, const T* src, const int64_t* from, const int64_t* to, int64_t dst, int delta, bool two,
+                    bool turn, int w, Scale sc) {
+        constexpr RopeKind kind = decltype(kind_c)::value;
+        constexpr bool E4M3 = sizeof(C) == 1 && kind != kRotateQuery;
+        for (int t0 = 0; t0 < n_tok; t0 += kRopeBatch) {
             V x[kRopeBatch][2];
-            int tt = i0 / per_tok, hk = i0 - tt * per_tok;
-            const int tt0 = tt, hk0 = hk;
 #pragma unroll
             for (int j = 0; j < kRopeBatch; ++j) {
-                const int h = h0 + hk * p.lanes + lane_h;
                 x[j][0] = V{};
                 x[j][1] = V{};
-                if (on && tt < n_tok && h < h_end && tokens[tt].live) {
-                    if (h < first_v) {
-                        const T* src = h < first_k ? static_cast<const T*>(p.q) + tokens[tt].q + h * p.qs.h
-                                                   : static_cast<const T*>(p.k) + tokens[tt].k + (h - first_k) * p.ks.h;
-                        x[j][0] = *reinterpret_cast<const V*>(src + c0);
-                        if (c1 < p.d) x[j][1] = *reinterpret_cast<const V*>(src + c1);
-                    } else {
-                        const int hv = (h - first_v) / p.vsub, wv = (h - first_v) % p.vsub * upq + w;
-                        const T* src = static_cast<const T*>(p.v) + tokens[tt].v + hv * p.vs.h + 2 * VE * wv;
-                        if (wv < upv) {
-                            x[j][0] = *reinterpret_cast<const V*>(src);
-                            if (2 * VE * wv + VE < p.dv) x[j][1] = *reinterpret_cast<const V*>(src + VE);
-                        }
-                    }
-                }
-                if (++hk == per_tok) {
-                    hk = 0;
-                    ++tt;
+                if (t0 + j < n_tok && at.live[t0 + j]) {
+                    const T* a = src + from[t0 + j];
+                    x[j][0] = *reinterpret_cast<const V*>(a);
+                    if (two) x[j][1] = *reinterpret_cast<const V*>(a + delta);
                 }
             }
-            if (!have_table) {
-                for (int i = threadIdx.x; i < n_tok * p.n; i += kRopeThreads) {
-                    const int k = i / p.n;
-                    const double turns = tokens[k].pos * (p.inv_freq[i - k * p.n] * 0.15915494309189533577);
-                    float sn, cn;
-                    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
-                    cs[k * p.n + table_at<VE>(i - k * p.n, p.n)] =
-                        make_float2(cn * p.amplitude, sn * p.amplitude * p.sign);
-                }
-                __syncthreads();
-                have_table = true;
-            }
-            tt = tt0;
-            hk = hk0;
 #pragma unroll
             for (int j = 0; j < kRopeBatch; ++j) {
-                const int h = h0 + hk * p.lanes + lane_h, at = tt;
-                if (++hk == per_tok) {
-                    hk = 0;
-                    ++tt;
+                const int k = t0 + j;
+                if (k >= n_tok || (kind != kRotateQuery && !at.store[k])) continue;
+                const int64_t o = to[k] + dst;
+                if constexpr (kind == kCopyValue && !E4M3) {  // the same type: the bits
+                    *reinterpret_cast<V*>(static_cast<C*>(p.vc) + o) = x[j][0];
+                    if (two) *reinterpret_cast<V*>(static_cast<C*>(p.vc) + o + delta) = x[j][1];
+                    continue;
                 }
-                if (!on || at >= n_tok || h >= h_end) continue;
-                const bool store = tokens[at].store;
-                if (h < first_v) {
-                    if (h >= first_k && !store) continue;
-                    float a[VE], c[VE];
-                    unpack<T, VE>(x[j][0], a);
-                    unpack<T, VE>(x[j][1], c);
-                    if (turn) {
-                        float2 r[VE];
+                float a[VE], c[VE];
+                unpack<T, VE>(x[j][0], a);
+                unpack<T, VE>(x[j][1], c);
+                if (kind != kCopyValue && turn && (kind == kRotateKey || at.live[k])) {
+                    float2 r[VE];
 #pragma unroll
-                        for (int i = 0; i < VE; i += 2) {
-                            const float2* from = cs + at * p.n + table_at<VE>(VE * w + i, p.n);
-                            if constexpr (VE == 1) {
-                                r[0] = from[0];
-                            } else {
-                                const float4 two = *reinterpret_cast<const float4*>(from);
-                                r[i] = make_float2(two.x, two.y);
-                                r[i + 1] = make_float2(two.z, two.w);
-                            }
-                        }
-                        if constexpr (INTER) {
-                            // pairs lie side by side in the 2 VE values
-                            float z[2 * VE];
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                z[i] = a[i];
-                                z[VE + i] = c[i];
-                            }
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                const float x0 = z[2 * i], x1 = z[2 * i + 1];
-                                z[2 * i] = x0 * r[i].x - x1 * r[i].y;
-                                z[2 * i + 1] = x1 * r[i].x + x0 * r[i].y;
-                            }
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                a[i] = z[i];
-                                c[i] = z[VE + i];
-                            }
+                    for (int i = 0; i < VE; i += 2) {
+                        const float2* tab = cs + k * p.n + table_at<VE>(VE * w + i, p.n);
+                        if constexpr (VE == 1) {
+                            r[0] = tab[0];
                         } else {
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                const float x0 = a[i], x1 = c[i];
-                                a[i] = x0 * r[i].x - x1 * r[i].y;
-                                c[i] = x1 * r[i].x + x0 * r[i].y;
-                            }
+                            const float4 pair = *reinterpret_cast<const float4*>(tab);
+                            r[i] = make_float2(pair.x, pair.y);
+                            r[i + 1] = make_float2(pair.z, pair.w);
                         }
                     }
-                    if (h < first_k) {
-                        if (!tokens[at].live) {  // zeros, whatever the table holds for the missing position
+                    if constexpr (INTER) {
+                        // pairs lie side by side in the 2 VE values
+                        float z[2 * VE];
 #pragma unroll
-                            for (int i = 0; i < VE; ++i) a[i] = c[i] = 0.f;
+                        for (int i = 0; i < VE; ++i) {
+                            z[i] = a[i];
+                            z[VE + i] = c[i];
                         }
-                        const int64_t o = tokens[at].out + h * p.os.h;
-                        store_vec<T, VE>(p.q_out, o + c0, a);
-                        if (c1 < p.d) store_vec<T, VE>(p.q_out, o + c1, c);
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) {
+                            const float x0 = z[2 * i], x1 = z[2 * i + 1];
+                            z[2 * i] = x0 * r[i].x - x1 * r[i].y;
+                            z[2 * i + 1] = x1 * r[i].x + x0 * r[i].y;
+                        }
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) {
+                            a[i] = z[i];
+                            c[i] = z[VE + i];
+                        }
                     } else {
-                        const int64_t o = tokens[at].cache + (h - first_k) * p.k_head;
-                        if constexpr (sizeof(C) == 1) {
-                            const Scale sc = make_scale(p.k_scale[p.scale_by_head ? h - first_k : 0]);
-                            store_e4m3<VE>(p.kc, o + c0, a, sc);
-                            if (c1 < p.d) store_e4m3<VE>(p.kc, o + c1, c, sc);
-                        } else {
-                            store_vec<C, VE>(p.kc, o + c0, a);
-                            if (c1 < p.d) store_vec<C, VE>(p.kc, o + c1, c);
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) {
+                            const float x0 = a[i], x1 = c[i];
+                            a[i] = x0 * r[i].x - x1 * r[i].y;
+                            c[i] = x1 * r[i].x + x0 * r[i].y;
                         }
                     }
-                } else if (store) {
-                    const int hv = (h - first_v) / p.vsub, wv = (h - first_v) % p.vsub * upq + w;
-                    if (wv >= upv) continue;
-                    const bool two = 2 * VE * wv + VE < p.dv;
-                    const int64_t o = tokens[at].cache + hv * p.v_head + 2 * VE * wv;
-                    if constexpr (sizeof(C) == 1) {
-                        float a[VE], c[VE];
-                        unpack<T, VE>(x[j][0], a);
-                        unpack<T, VE>(x[j][1], c);
-                        const Scale sc = make_scale(p.v_scale[p.scale_by_head ? hv : 0]);
-                        store_e4m3<VE>(p.vc, o, a, sc);
-                        if (two) store_e4m3<VE>(p.vc, o + VE, c, sc);
-                    } else {  // the same type: the bits
-                        *reinterpret_cast<V*>(static_cast<C*>(p.vc) + o) = x[j][0];
-                        if (two) *reinterpret_cast<V*>(static_cast<C*>(p.vc) + o + VE) = x[j][1];
-                    }
                 }
+                if constexpr (E4M3) {
+                    void* base = kind == kRotateKey ? p.kc : p.vc;
+                    store_e4m3<VE>(base, o, a, sc);
+                    if (two) store_e4m3<VE>(base, o + delta, c, sc);
+                } else if constexpr (kind == kRotateKey) {
+                    store_vec<C, VE>(p.kc, o, a);
+                    if (two) store_vec<C, VE>(p.kc, o + delta, c);
+                } else {
+                    store_vec<T, VE>(p.q_out, o, a);
+                    if (two) store_vec<T, VE>(p.q_out, o + delta, c);
+                }
+            }
+        }
+    };
+    // one pass unless a head has more units than the block has threads
+    for (int w = threadIdx.x % p.width; w < upq; w += p.width) {
+        const bool turn = w < nrot;
+        // columns of the unit's two vectors in a q or k head
+        const int c0 = turn ? (INTER ? 2 * VE * w : VE * w) : 2 * p.n + 2 * VE * (w - nrot);
+        const int delta = turn && !INTER ? p.n : VE;
+        const bool two = c0 + delta < p.d;
+        for (int h = h0 + lane_h; h < h_end; h += p.lanes) {
+            if (h < first_k) {
+                walk(std::integral_constant<RopeKind, kRotateQuery>{}, static_cast<const T*>(p.q) + h * p.qs.h + c0, at.q,
+                     at.out, h * p.os.h + c0, delta, two, turn, w, Scale{});
+            } else if (h < first_v) {
+                const int hk = h - first_k;
+                const Scale sc = sizeof(C) == 1 ? make_scale(p.k_scale[p.scale_by_head ? hk : 0]) : Scale{};
+                walk(std::integral_constant<RopeKind, kRotateKey>{}, static_cast<const T*>(p.k) + hk * p.ks.h + c0, at.k,
+                     at.cache, hk * p.k_head + c0, delta, two, turn, w, sc);
+            } else {
+                const int hv = (h - first_v) / p.vsub, wv = (h - first_v) % p.vsub * upq + w;
+                if (wv >= upv) continue;
+                const Scale sc = sizeof(C) == 1 ? make_scale(p.v_scale[p.scale_by_head ? hv : 0]) : Scale{};
+                walk(std::integral_constant<RopeKind, kCopyValue>{}, static_cast<const T*>(p.v) + hv * p.vs.h + 2 * VE * wv,
+                     at.v, at.cache, hv * p.v_head + 2 * VE * wv, VE, 2 * VE * wv + VE < p.dv, false, w, sc);
             }
         }
     }
