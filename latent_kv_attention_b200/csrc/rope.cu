@@ -58,7 +58,10 @@ struct RopeParams {
 
 namespace {
 
-constexpr int kRopeThreads = 128, kRopeBlocks = 7;  // per SM
+constexpr int kRopeThreads = 128;
+// Blocks per SM: as many as the registers of four units in flight allow without spilling.
+template <typename C>
+constexpr int rope_blocks() { return sizeof(C) == 1 ? 5 : 6; }
 constexpr int kRopeBatch = 4;  // units in flight per thread
 constexpr int kRopeMaxPairs = 256;
 constexpr int kRopeMaxTokens = 8, kRopeTable = 512;  // tokens per CTA, (cos, sin) pairs of its tables
@@ -147,7 +150,7 @@ enum RopeKind { kRotateQuery, kRotateKey, kCopyValue };
 
 // T: element of q, k, v and q_out; C: element of the cache; VE: values per vector (1: no alignment needed).
 template <typename T, typename C, int VE, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, rope_blocks<C>()) rope_kernel(const RopeParams p) {
     using V = typename VecOf<T, VE>::V;
     __shared__ __align__(16) float2 cs[kRopeTable];
     __shared__ RopeTokens at;
@@ -341,7 +344,7 @@ cudaError_t rope_launch(RopeParams& p, bool inter, cudaStream_t st) {
     // Many tokens: several per CTA, as many as the tables hold, such that the CTAs fill whole waves; few: one head per
     // thread, spread over the SMs.
     p.heads_per_cta = p.vheads;
-    const long long slots = (long long)kRopeBlocks * sm_count(), most = std::min(kRopeMaxTokens, kRopeTable / p.n);
+    const long long slots = (long long)rope_blocks<C>() * sm_count(), most = std::min(kRopeMaxTokens, kRopeTable / p.n);
     const long long waves = (tokens + slots * most - 1) / (slots * most);
     p.tokens_per_cta = (int)((tokens + slots * waves - 1) / (slots * waves));
     if (tokens < 4LL * sm_count()) {
