@@ -96,7 +96,8 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float* f
 
 // A per-head scale of an e4m3 cache and how to divide by it.  For scales of ordinary size x / s is the product with the
 // rounded reciprocal r and one correction, q + (x - q s) r: the correctly rounded quotient (Markstein's theorem) in
-// three operations; for others, and for infinite quotients, the division itself.
+// three operations; for others, and for infinite quotients, the division itself, out of line (inlined for every value
+// it pushed the loop out of the instruction cache).
 struct Scale {
     float s, r;
     bool plain;
@@ -104,23 +105,31 @@ struct Scale {
 __device__ __forceinline__ Scale make_scale(float s) {
     return {s, __frcp_rn(s), fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f};
 }
-__device__ __forceinline__ float quotient(float x, const Scale& c) {
-    if (!c.plain) return __fdiv_rn(x, c.s);
-    const float q = __fmul_rn(x, c.r), e = __fmaf_rn(-q, c.s, x);
-    return fabsf(q) < 0x1p100f ? __fmaf_rn(e, c.r, q) : q;
-}
+__device__ __noinline__ float divide(float x, float s) { return __fdiv_rn(x, s); }
 // VE values as e4m3 of value / scale, rounded to nearest even and saturated.
 template <int VE>
 __device__ __forceinline__ void store_e4m3(void* base, int64_t at, const float* f, const Scale& c) {
     uint8_t* p = static_cast<uint8_t*>(base) + at;
+    float q[VE], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+        q[i] = __fmul_rn(f[i], c.r);
+        most = fmaxf(most, fabsf(q[i]));
+    }
+    if (c.plain && most < 0x1p100f) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) q[i] = __fmaf_rn(__fmaf_rn(-q[i], c.s, f[i]), c.r, q[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) q[i] = divide(f[i], c.s);
+    }
     if constexpr (VE == 1) {
-        *p = (uint8_t)__nv_cvt_float_to_fp8(quotient(f[0], c), __NV_SATFINITE, __NV_E4M3);
+        *p = (uint8_t)__nv_cvt_float_to_fp8(q[0], __NV_SATFINITE, __NV_E4M3);
     } else {
         uint16_t b[VE / 2];
 #pragma unroll
         for (int i = 0; i < VE; i += 2)
-            b[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(f[i], c), quotient(f[i + 1], c)), __NV_SATFINITE,
-                                                __NV_E4M3);
+            b[i / 2] = __nv_cvt_float2_to_fp8x2(make_float2(q[i], q[i + 1]), __NV_SATFINITE, __NV_E4M3);
         if constexpr (VE == 8)
             *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(b);
         else

@@ -252,6 +252,22 @@ def test_latent_append(kind, page, r_kv, d_r):
         assert torch.equal(got[b, rest], old[b, rest])
 
 
+def test_e4m3_append_of_extreme_values_and_scales():
+    """Values and scales of every size divide as the fp32 division does: infinities and overflows saturate to 448, NaN
+    stays NaN, a zero scale gives what division by zero gives."""
+    x = torch.tensor([0.0, -0.0, 1.0, -1.0, 3e38, -3e38, math.inf, -math.inf, math.nan, 1e-38, 7.5, 0.013, 448.0, 464.0, 1e30, -2e-3],
+                     device=DEV).to(torch.bfloat16)
+    v = x.view(1, 1, 1, 16).expand(1, 6, 1, 16).contiguous()
+    scale = torch.tensor([1.0, 1e-38, 3e38, 0.0, 0.0123, 1e25], device=DEV)
+    f, _ = lka.rope_inv_freq(2)
+    caches = [torch.zeros(1, 6, 8, 16, dtype=torch.uint8, device=DEV).view(E4M3) for _ in range(2)]
+    lka.gqa_rope_append_fp8kv(v, v, v, *caches, scale, scale, ints(1), f)
+    want = (v.float() / scale[None, :, None, None])[0, :, 0]
+    got = caches[1][0, :, 0].float()
+    want8 = want.clamp(-448, 448).to(E4M3).float()
+    assert torch.equal(got.isnan(), want8.isnan()) and torch.equal(got.nan_to_num(1.0), want8.nan_to_num(1.0))
+
+
 def test_append_reports_bad_lengths_and_pages():
     g = gen(3)
     q, k = randn(g, 3, 4, 2, 64), randn(g, 3, 2, 2, 64)
