@@ -43,8 +43,8 @@ __device__ __forceinline__ RowWalk row_walk(const KeyWeightParams& p, int j0, in
 // memory 16 bytes a lane; the query rows pass through shared memory as columns, 8 at a time.  The head dim is
 // contracted in an order of its own, the same for both operands: in 32-value group j, lane column t brings values
 // 32 j + 8 t .. + 7, the first four to k-step 2j, the last four to 2j + 1.
-// A decode step is bound by reading the keys (D bytes per key and row of the group are 2 / ratio of a FLOP each);
-// a block of 64 keys is 16 KB at D = 128, small enough for many blocks per SM.
+// A decode step is bound by reading the keys: a warp walks `groups` groups of 16 keys and has the next group's loads
+// (4 KB at D = 128) under way while it works on this one.
 template <int D>
 __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightParams p) {
     constexpr int NJ = D / 32;
@@ -53,31 +53,33 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
     const int chunk = p.chunk;
     uint8_t* qs = smem;                                                    // [2][chunk][QROW]
     float* ls = reinterpret_cast<float*>(smem + 2 * (size_t)chunk * QROW);  // [2][chunk] log2 normalisers
-    const int j0 = blockIdx.x * kTile, kvh = blockIdx.y, b = blockIdx.z;
+    const int kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int L = clamp_len(p.lens, b, p.Lmax, p.s, p.causal, p.status, threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0);
     const size_t wrow = ((size_t)b * p.h_kv + kvh) * p.Lmax;
-    if (j0 >= L) {
-        const int j = j0 + threadIdx.x;
-        if (threadIdx.x < kTile && j < p.Lmax && !p.accumulate) p.w[wrow + j] = 0.f;
-        return;
-    }
-    // the warp's keys
-    const int key[2] = {j0 + warp * 16 + g, j0 + warp * 16 + g + 8};
-    uint4 kr[2][NJ];
+    const int first_tile = blockIdx.x * p.groups, block0 = first_tile * kTile;
+    if (!p.accumulate)  // the block's keys past the length
+        for (int j = max(block0, L) + threadIdx.x; j < min(block0 + p.groups * kTile, p.Lmax); j += 128) p.w[wrow + j] = 0.f;
+    if (block0 >= L) return;
+    const int n_tiles = min(p.groups, cdiv(L - block0, kTile));
     const CacheRows rows{p.table ? p.table + (size_t)b * p.max_pages : nullptr, p.page_size, p.num_pages,
                          p.table ? (long long)kvh : ((long long)b * p.h_kv + kvh) * p.Lmax, p.h_kv};
+    // this lane's two keys of a tile: rows g and g + 8 of the warp's 16
+    auto load_keys = [&](int j0, uint4 (*to)[NJ]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const bool ok = key[h] < L;
-        const __nv_bfloat16* src =
-            static_cast<const __nv_bfloat16*>(p.k) + (ok ? cache_row(rows, key[h], p.status) : 0) * D;
+        for (int h = 0; h < 2; ++h) {
+            const int key = j0 + warp * 16 + g + 8 * h;
+            const bool ok = key < L;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k) + (ok ? cache_row(rows, key, p.status) : 0) * D;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            kr[h][j] = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * t)) : make_uint4(0, 0, 0, 0);
-    }
+            for (int j = 0; j < NJ; ++j)
+                to[h][j] = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * t)) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    uint4 kr[2][NJ], kn[2][NJ];
+    load_keys(block0, kr);
 
-    const RowWalk walk = row_walk(p, j0, L);
+    const RowWalk walk = row_walk(p, block0, L);
     const int per_seg = cdiv(max(walk.len - walk.start, 0), chunk), n_chunks = walk.segs * per_seg;
     const size_t row0 = ((size_t)b * p.h_q + (size_t)kvh * p.ratio) * p.s;
     auto chunk_at = [&](int c, int& first, int& n) {  // rows [first, first + n) of the group
@@ -101,60 +103,65 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
         }
         cp_async_commit();
     };
-    float w[2] = {0.f, 0.f};
+    // Several tiles per block only where all rows are one chunk (kernel launch); otherwise one tile and all chunks.
     if (n_chunks > 0) stage(0);
-    for (int c = 0; c < n_chunks; ++c) {
-        if (c + 1 < n_chunks) {
-            stage(c + 1);
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
-        }
-        __syncthreads();
-        int first, n;
-        chunk_at(c, first, n);
-        const uint8_t* qb = qs + (size_t)(c & 1) * chunk * QROW;
-        const float* lb = ls + (c & 1) * chunk;
-        // queries of this chunk that may not see every key of the tile need the mask
-        const bool masked = (p.causal && j0 + kTile - 1 > L - p.s + (p.s < kTile ? 0 : first % p.s)) || j0 + kTile > L;
-#pragma unroll 2
-        for (int r0 = 0; r0 < n; r0 += 8) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint8_t* qrow = qb + (r0 + g) * QROW + t * 16;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const uint4 qv = *reinterpret_cast<const uint4*>(qrow + j * 64);
-                const uint32_t a0[4] = {kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y};
-                const uint32_t a1[4] = {kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w};
-                mma_bf16(acc, a0, qv.x, qv.y);
-                mma_bf16(acc, a1, qv.z, qv.w);
-            }
-            const float2 l2 = *reinterpret_cast<const float2*>(lb + r0 + 2 * t);
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = fast_exp2(fmaf(acc[i], p.scale_log2, i & 1 ? -l2.y : -l2.x));
-            if (masked || r0 + 8 > n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + 2 * t + (i & 1), kj = key[i / 2];
-                    const int last = p.causal ? L - p.s + (first + r) % p.s : L - 1;
-                    if (r >= n || kj > last) e[i] = 0.f;
+    for (int tile = 0; tile < n_tiles; ++tile) {
+        const int j0 = block0 + tile * kTile;
+        if (tile + 1 < n_tiles) load_keys(j0 + kTile, kn);
+        float w[2] = {0.f, 0.f};
+        for (int c = 0; c < n_chunks; ++c) {
+            if (tile == 0) {
+                if (c + 1 < n_chunks) {
+                    stage(c + 1);
+                    cp_async_wait<1>();
+                } else {
+                    cp_async_wait<0>();
                 }
+                __syncthreads();
             }
-            w[0] += e[0] + e[1];
-            w[1] += e[2] + e[3];
-        }
-        __syncthreads();
-    }
+            int first, n;
+            chunk_at(c, first, n);
+            const uint8_t* qb = qs + (size_t)(c & 1) * chunk * QROW;
+            const float* lb = ls + (c & 1) * chunk;
+            // queries of this chunk that may not see every key of the tile need the mask
+            const bool masked = (p.causal && j0 + kTile - 1 > L - p.s + (p.s < kTile ? 0 : first % p.s)) || j0 + kTile > L;
+#pragma unroll 2
+            for (int r0 = 0; r0 < n; r0 += 8) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint8_t* qrow = qb + (r0 + g) * QROW + t * 16;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] += __shfl_xor_sync(0xffffffffu, w[h], 1);
-        w[h] += __shfl_xor_sync(0xffffffffu, w[h], 2);
-        if (t == 0) {
-            if (key[h] < L)
-                write_weight(p, wrow + key[h], w[h]);
-            else if (key[h] < p.Lmax && !p.accumulate)
-                p.w[wrow + key[h]] = 0.f;
+                for (int j = 0; j < NJ; ++j) {
+                    const uint4 qv = *reinterpret_cast<const uint4*>(qrow + j * 64);
+                    const uint32_t a0[4] = {kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y};
+                    const uint32_t a1[4] = {kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w};
+                    mma_bf16(acc, a0, qv.x, qv.y);
+                    mma_bf16(acc, a1, qv.z, qv.w);
+                }
+                const float2 l2 = *reinterpret_cast<const float2*>(lb + r0 + 2 * t);
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = fast_exp2(fmaf(acc[i], p.scale_log2, i & 1 ? -l2.y : -l2.x));
+                if (masked || r0 + 8 > n) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + 2 * t + (i & 1), key = j0 + warp * 16 + g + 8 * (i / 2);
+                        const int last = p.causal ? L - p.s + (first + r) % p.s : L - 1;
+                        if (r >= n || key > last) e[i] = 0.f;
+                    }
+                }
+                w[0] += e[0] + e[1];
+                w[1] += e[2] + e[3];
+            }
+            if (n_chunks > 1) __syncthreads();
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[h] += __shfl_xor_sync(0xffffffffu, w[h], 1);
+            w[h] += __shfl_xor_sync(0xffffffffu, w[h], 2);
+            const int key = j0 + warp * 16 + g + 8 * h;
+            if (t == 0 && key < L) write_weight(p, wrow + key, w[h]);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) kr[h][j] = kn[h][j];
         }
     }
 }
@@ -232,10 +239,15 @@ __global__ void __launch_bounds__(128) key_weights_f32_kernel(const KeyWeightPar
 }
 
 template <int D>
-cudaError_t launch_mma(KeyWeightParams p, const dim3& grid, cudaStream_t st) {
+cudaError_t launch_mma(KeyWeightParams p, dim3 grid, cudaStream_t st) {
     // whole groups of 8 rows; 64 rows at a time hide the copies of the next ones behind 8 MMA column groups
     p.chunk = std::min(64, cdiv(p.ratio * p.s, 8) * 8);
     const int smem = 2 * p.chunk * (D * 2 + 64 + 4);
+    // several tiles of keys per block, for the loads ahead, where the rows are one chunk and the blocks stay many
+    p.groups = 1;
+    if (p.ratio * p.s <= p.chunk)
+        while (p.groups < 8 && (long long)grid.y * grid.z * cdiv(p.Lmax, kTile * p.groups * 2) >= 8LL * sm_count()) p.groups *= 2;
+    grid.x = cdiv(p.Lmax, kTile * p.groups);
     const cudaError_t e = allow_smem<key_weights_mma_kernel<D>>(2 * 64 * (D * 2 + 64 + 4));
     if (e != cudaSuccess) return e;
     TimedLaunch timer(st);

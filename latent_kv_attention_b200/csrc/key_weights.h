@@ -17,6 +17,7 @@ struct KeyWeightParams {
     int B, h_q, h_kv, s, Lmax, causal, accumulate, ratio;
     int page_size, max_pages, num_pages;
     int chunk;            // query rows staged at a time (a multiple of 8)
+    int groups;           // tiles of keys per block
     float scale_log2;
 };
 
