@@ -20,6 +20,7 @@ import torch
 from . import _DT, _check, library, workspaces
 
 _E4M3 = torch.float8_e4m3fn
+_Tensor = torch.Tensor
 _CACHE_DT = {torch.bfloat16: 0, torch.float32: 1, _E4M3: 2}
 _HEADER = 256  # bytes of a workspace that hold the status word
 
@@ -56,7 +57,8 @@ def _code(t, name):
 
 
 def _dense(t, name, dtype, device, shape=None):
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous() and
+    """The address of a contiguous tensor of this type, device and shape."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous() and
             (shape is None or t.shape == shape)):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}" +
                          (f" of shape {list(shape)}" if shape is not None else ""))
@@ -89,6 +91,8 @@ def _table(block_table, B, device):
 
 _I3, _I9 = ctypes.c_int64 * 3, ctypes.c_int64 * 9
 _functions = {}
+_device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _function(name):
@@ -101,33 +105,29 @@ def _function(name):
 def _call(name, device, args, scratch=_HEADER):
     """Calls the library on the device's current stream, with a workspace of `scratch` bytes after `args` (none if
     scratch is 0).  A captured call gets its scratch from the graph's memory."""
-    f, index = _function(name), device.index
-    before = torch._C._cuda_getDevice()
-    if before != index:
-        torch.cuda.set_device(index)
-    try:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-        if scratch == 0:
-            rc = f(*args, stream)
-        elif not torch.cuda.is_current_stream_capturing():
-            if index not in _captured:
-                captured_status(device, create=True)  # outside a graph, so that no replay clears it
-            ws = workspaces._ws.get((index, stream))
-            if ws is None or ws.numel() < scratch:
-                ws = workspaces.get(scratch, device)
-            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
-        elif scratch <= _HEADER:
-            ws = captured_status(device, create=True)
-            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
-        else:
-            ws = torch.empty(scratch, dtype=torch.uint8, device=device)
-            ws[:_HEADER].zero_()
-            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
-            # the captured call's flags outlive its scratch
-            captured_status(device, create=True)[:4].view(torch.int32).bitwise_or_(ws[:4].view(torch.int32))
-    finally:
-        if before != index:
-            torch.cuda.set_device(before)
+    index = device.index
+    if _device_now() != index:
+        with torch.cuda.device(device):
+            return _call(name, device, args, scratch)
+    f, stream = _function(name), _stream_now(index)
+    if scratch == 0:
+        rc = f(*args, stream)
+    elif not _capturing():
+        if index not in _captured:
+            captured_status(device, create=True)  # outside a graph, so that no replay clears it
+        ws = workspaces._ws.get((index, stream))
+        if ws is None or ws.numel() < scratch:
+            ws = workspaces.get(scratch, device)
+        rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+    elif scratch <= _HEADER:
+        ws = captured_status(device, create=True)
+        rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+    else:
+        ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+        ws[:_HEADER].zero_()
+        rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+        # the captured call's flags outlive its scratch
+        captured_status(device, create=True)[:4].view(torch.int32).bitwise_or_(ws[:4].view(torch.int32))
     if rc:
         _check(name, rc)
 

@@ -291,27 +291,35 @@ struct MovePlan {
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, const MovePlan m) {
     const int h = blockIdx.y, b = blockIdx.z;
-    const int L = evict_len(p, b, false), n = min(L, p.budget);
     const int range = blockIdx.x % m.ranges, what = blockIdx.x / m.ranges;
-    const int per = cdiv(n, m.ranges), r0 = min(n, range * per), r1 = min(n, r0 + per);
     const int32_t* kept = p.kept + ((size_t)b * p.h_kv + h) * p.budget;
     const int64_t bh = (int64_t)b * p.h_kv + h;
     pdl_wait();
     if (what == 2 * m.slices) {  // the weights; the places behind the kept keys start from nothing
+        const int n = min(evict_len(p, b, false), p.budget);
+        const int per = cdiv(n, m.ranges), r0 = min(n, range * per), r1 = min(n, r0 + per);
         move_rows<float, IN_PLACE>(p, reinterpret_cast<const uint8_t*>(p.w), reinterpret_cast<uint8_t*>(p.wo), bh * p.Lmax,
-                         bh * p.Lout, nullptr, 4, 0, 1, kept, r0, r1);
+                                   bh * p.Lout, nullptr, 4, 0, 1, kept, r0, r1);
         const int z = p.Lout - n, zper = cdiv(z, m.ranges);
         for (int i = n + range * zper + threadIdx.x; i < min(p.Lout, n + (range + 1) * zper); i += kMoveThreads)
             p.wo[bh * p.Lout + i] = 0.f;
         return;
     }
-    if (IN_PLACE && L <= p.budget) return;  // in place, and nothing leaves
     const bool is_v = what >= m.slices;
     const int col = (what - (is_v ? m.slices : 0)) * m.slice;
     const int bytes = min(m.slice, p.row_bytes - col);
-    const CacheRows rows{p.table ? p.table + (size_t)b * p.max_pages : nullptr, p.page_size, p.num_pages, h, p.h_kv};
-    move_rows<uint4, IN_PLACE>(p, is_v ? p.v : p.k, is_v ? p.vo : p.ko, bh * p.Lmax, bh * p.Lout, p.table ? &rows : nullptr,
-                     p.row_bytes, col, bytes / 16, kept, r0, r1);
+    if constexpr (IN_PLACE) {
+        const int L = evict_len(p, b, false);
+        if (L <= p.budget) return;  // nothing leaves
+        const CacheRows rows{p.table ? p.table + (size_t)b * p.max_pages : nullptr, p.page_size, p.num_pages, h, p.h_kv};
+        move_rows<uint4, true>(p, is_v ? p.v : p.k, is_v ? p.vo : p.ko, bh * p.Lmax, bh * p.Lout, p.table ? &rows : nullptr,
+                               p.row_bytes, col, bytes / 16, kept, 0, p.budget);
+    } else {
+        // the list itself says where the kept rows end
+        const int per = cdiv(p.budget, m.ranges), r0 = min(p.budget, range * per);
+        move_rows<uint4, false>(p, is_v ? p.v : p.k, is_v ? p.vo : p.ko, bh * p.Lmax, bh * p.Lout, nullptr, p.row_bytes, col,
+                                bytes / 16, kept, r0, min(p.budget, r0 + per));
+    }
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
