@@ -5,8 +5,9 @@
 // lane) and streams tiles of 128 query rows of the group's heads (the columns) through a TMA
 // ring.  A key's weight is a sum along its own lane, so nothing crosses lanes and no P is
 // written back: per score one multiply-add with the row's normaliser, one exponential, one
-// addition.  Warp 16 loads, warp 17 issues the MMAs into four score buffers of tensor memory,
-// four groups of four warps take the score tiles in turn.  With few key tiles, the query tiles of one
+// addition.  Warp 16 loads, three threads issue the MMAs into four score buffers of tensor memory
+// (one alone took 1400 cycles per tile, most of it waits and commits), four groups of four
+// warps take the score tiles in turn.  With few key tiles, the query tiles of one
 // key tile are dealt to the CTAs of a cluster, whose sums rank 0 adds in order.
 //
 // Bound: 16,384 exponentials per tile are 1024 cycles of the special-function unit (16 per
@@ -25,7 +26,8 @@ namespace lka {
 
 namespace kwt {
 constexpr int TK = 128, TQ = 128, NBUF = 4;
-constexpr int NG = 4, NT = 32 * (4 * NG + 2);  // groups of four warps, one per score buffer
+constexpr int NG = 4, NM = 3;                 // groups of four softmax warps, one per score buffer; MMA issuers
+constexpr int W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, NT = 32 * (W_MMA + NM);
 template <int D>
 struct Cfg {
     static constexpr int NB = D / 64, BOX = 128 * 128, TILE = NB * BOX;
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
         }
         fence_barrier_init();
     }
-    if (warp == 4 * NG + 1) {
+    if (warp == W_LOAD) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 4 * NG) {
+    if (warp == W_LOAD) {
         if (lane == 0) {
             const uint32_t kb = smem_u32(k_full);
             mbar_arrive_expect_tx(kb, C::TILE);
@@ -151,27 +153,29 @@ __global__ void __launch_bounds__(kwt::NT, 1)
                 mbar_wait(smem_u32(&full[i % C::NS]), (i / C::NS) & 1, p.status);
             mbar_wait(kb, 0, p.status);
         }
-    } else if (warp == 4 * NG + 1) {
-        constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-        bool ok = mbar_wait(smem_u32(k_full), 0, p.status);
-        for (int i = 0; ok && i < n_mine; ++i) {
-            const int s = i % C::NS, buf = i % NBUF;
-            ok = mbar_wait(smem_u32(&full[s]), (i / C::NS) & 1, p.status);
-            if (ok && i >= NBUF) ok = mbar_wait(smem_u32(&s_free[buf]), (i / NBUF - 1) & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t ka = smem_u32(smem), qa = smem_u32(smem + C::OFF_Q + s * C::TILE);
+    } else if (warp >= W_MMA) {
+        // MMA issuers: one thread per warp, every NM-th tile each
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+            constexpr int B4 = C::BOX >> 4;
+            const uint64_t kd = smem_desc_sw128(smem_u32(smem), 16, 1024);
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+            bool ok = mbar_wait(smem_u32(k_full), 0, p.status);
+            for (int i = warp - W_MMA; ok && i < n_mine; i += NM) {
+                const int s = i % C::NS, buf = i % NBUF;
+                ok = mbar_wait(smem_u32(&full[s]), (i / C::NS) & 1, p.status);
+                if (ok && i >= NBUF) ok = mbar_wait(smem_u32(&s_free[buf]), (i / NBUF - 1) & 1, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t qd = q_desc + (uint64_t)(s * (C::TILE >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_ss(tmem + buf * 128, smem_desc_sw128(ka + (k / 4) * C::BOX + (k % 4) * 32, 16, 1024),
-                            smem_desc_sw128(qa + (k / 4) * C::BOX + (k % 4) * 32, 16, 1024), idesc, k != 0);
+                    umma_ss(tmem + buf * 128, kd + (k / 4) * B4 + (k % 4) * 2, qd + (k / 4) * B4 + (k % 4) * 2, idesc, k != 0);
                 umma_commit(smem_u32(&s_ready[buf]));
                 umma_commit(smem_u32(&empty[s]));
             }
-            __syncwarp();
+            if (!ok) s_abort = 1;
         }
-        if (!ok) s_abort = 1;
     } else {
         const int grp = warp / 4, r = threadIdx.x % 128;  // the key's tensor-memory lane, and the row whose lse it stages
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4 * NG + 1) tmem_dealloc(tmem, 512);
+    if (warp == W_LOAD) tmem_dealloc(tmem, 512);
     if (cluster > 1) cluster_sync();
     if (rank == 0 && threadIdx.x < TK) {
         const int key = j0 + threadIdx.x;
