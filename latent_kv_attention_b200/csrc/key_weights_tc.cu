@@ -5,13 +5,17 @@
 // lane) and streams tiles of 128 query rows of the group's heads (the columns) through a TMA
 // ring.  A key's weight is a sum along its own lane, so nothing crosses lanes and no P is
 // written back: per score one multiply-add with the row's normaliser, one exponential, one
-// addition.  Warp 16 loads, three threads issue the MMAs into four score buffers of tensor memory
-// (one alone took 1400 cycles per tile, most of it waits and commits), four groups of four
-// warps take the score tiles in turn.  With few key tiles, the query tiles of one
-// key tile are dealt to the CTAs of a cluster, whose sums rank 0 adds in order.
+// addition.  Warp 8 loads, warp 9 issues the MMAs into two score buffers of tensor memory, two
+// groups of four warps take the score tiles in turn; two CTAs per SM cover each other's starts
+// and waits.  With few key tiles, the query tiles of one key tile are dealt to the CTAs of a
+// cluster, whose sums rank 0 adds in order.
 //
 // Bound: 16,384 exponentials per tile are 1024 cycles of the special-function unit (16 per
-// cycle and SM) against 520 of the tensor pipe at d = 128.
+// cycle and SM) against 520 of the tensor pipe at d = 128.  Measured after a causal prompt of
+// 4096 tokens, 32 / 8 heads of 128 (16,896 tiles): 97 us, the unit about 0.7 busy.  The same in
+// one CTA per SM with four groups and one issuing thread 101 us (that thread's 1400 cycles per
+// tile), with three issuing threads 102-106; a quarter or three eighths of the exponentials as
+// polynomials on the FMA pipe 100-112 in every layout.
 #include <math.h>
 
 #include <algorithm>
@@ -25,17 +29,17 @@
 namespace lka {
 
 namespace kwt {
-constexpr int TK = 128, TQ = 128, NBUF = 4;
-constexpr int NG = 4, NM = 3;                 // groups of four softmax warps, one per score buffer; MMA issuers
-constexpr int W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, NT = 32 * (W_MMA + NM);
+constexpr int TK = 128, TQ = 128, NBUF = 2;
+constexpr int NG = 2, W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, NT = 32 * (W_MMA + 1);  // groups of four warps, one per buffer
 template <int D>
 struct Cfg {
     static constexpr int NB = D / 64, BOX = 128 * 128, TILE = NB * BOX;
-    static constexpr int NS = 4;  // query tiles in flight
+    static constexpr int NS = D == 128 ? 2 : 4;  // query tiles in flight
     static constexpr int OFF_Q = TILE, OFF_LSE = OFF_Q + NS * TILE;
-    static constexpr int OFF_SUM = OFF_LSE + 2 * NG * TQ * 4;  // [NG][2 parities][TQ]
+    static constexpr int OFF_SUM = OFF_LSE + 2 * 4 * NG * TQ * 4;  // [softmax warp][2 parities][TQ]
     static constexpr int OFF_BAR = OFF_SUM + NG * TK * 4;      // [NG][TK]
     static constexpr int SMEM = 1024 + OFF_BAR + 256;
+    static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
 };
 }  // namespace kwt
 
@@ -56,7 +60,7 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kwt::NT, 1)
+__global__ void __launch_bounds__(kwt::NT, 2)
     key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const KeyWeightParams p, const int cluster, const int box_rows) {
     using namespace kwt;
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
         fence_barrier_init();
     }
     if (warp == W_LOAD) {
-        tmem_alloc(tmem_slot, 512);
+        tmem_alloc(tmem_slot, NBUF * TQ);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -153,15 +157,14 @@ __global__ void __launch_bounds__(kwt::NT, 1)
                 mbar_wait(smem_u32(&full[i % C::NS]), (i / C::NS) & 1, p.status);
             mbar_wait(kb, 0, p.status);
         }
-    } else if (warp >= W_MMA) {
-        // MMA issuers: one thread per warp, every NM-th tile each
+    } else if (warp == W_MMA) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
             constexpr int B4 = C::BOX >> 4;
             const uint64_t kd = smem_desc_sw128(smem_u32(smem), 16, 1024);
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
             bool ok = mbar_wait(smem_u32(k_full), 0, p.status);
-            for (int i = warp - W_MMA; ok && i < n_mine; i += NM) {
+            for (int i = 0; ok && i < n_mine; ++i) {
                 const int s = i % C::NS, buf = i % NBUF;
                 ok = mbar_wait(smem_u32(&full[s]), (i / C::NS) & 1, p.status);
                 if (ok && i >= NBUF) ok = mbar_wait(smem_u32(&s_free[buf]), (i / NBUF - 1) & 1, p.status);
@@ -177,34 +180,37 @@ __global__ void __launch_bounds__(kwt::NT, 1)
             if (!ok) s_abort = 1;
         }
     } else {
-        const int grp = warp / 4, r = threadIdx.x % 128;  // the key's tensor-memory lane, and the row whose lse it stages
+        const int grp = warp / 4, r = threadIdx.x % 128;  // the key's tensor-memory lane
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
-        float* ls = reinterpret_cast<float*>(smem + C::OFF_LSE) + grp * 2 * TQ;
+        float* ls = reinterpret_cast<float*>(smem + C::OFF_LSE) + warp * 2 * TQ;
         const size_t row0 = ((size_t)b * p.h_q + (size_t)kvh * p.ratio) * p.s;
         const int key = j0 + r;
-        // log2 normaliser of row r of this CTA's tile i; +inf (nothing is added) past the head's queries and for rows
-        // that saw no key
-        auto lse_of = [&](int i) {
-            const int n = (int)rank + i * cluster, t = start + n % per * TQ + r;
-            if (i >= n_mine || t >= p.s) return INFINITY;
-            const float l = p.lse[row0 + (size_t)(n / per) * p.s + t];
-            return l == -INFINITY ? INFINITY : l * kLog2e;
+        // Every warp stages the negated log2 normalisers of a tile's rows for itself, a tile ahead (one copy per group
+        // needed a barrier per tile, whose skew cost a quarter of the time): -inf (nothing is added) past the head's
+        // queries and for rows that saw no key.
+        float next[TQ / 32];
+        auto fetch = [&](int i) {
+            const int n = (int)rank + i * cluster, head = n / per, t0 = start + (n - head * per) * TQ;
+#pragma unroll
+            for (int k = 0; k < TQ / 32; ++k) {
+                const int t = t0 + 32 * k + lane;
+                next[k] = INFINITY;
+                if (i < n_mine && t < p.s) next[k] = p.lse[row0 + (size_t)head * p.s + t];
+            }
         };
-        float next = lse_of(grp);
+        fetch(grp);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-        // one score tile, 32 columns at a time; MASK: rows before `first` do not see the key
+        // one score tile, 16 columns at a time; MASK: rows before `first` do not see the key
         auto tile = [&](auto mask, uint32_t ts, const float* lb, int first, uint32_t release) {
             constexpr bool MASK = decltype(mask)::value;
-            uint32_t sr[2][32];
+            uint32_t sr[2][16];
             tmem_ld16(ts, sr[0]);
-            tmem_ld16(ts + 16, sr[0] + 16);
 #pragma unroll
-            for (int q = 0; q < TQ / 32; ++q) {
+            for (int q = 0; q < TQ / 16; ++q) {
                 tmem_ld_wait();
-                if (q + 1 < TQ / 32) {
-                    tmem_ld16(ts + 32 * (q + 1), sr[(q + 1) & 1]);
-                    tmem_ld16(ts + 32 * (q + 1) + 16, sr[(q + 1) & 1] + 16);
+                if (q + 1 < TQ / 16) {
+                    tmem_ld16(ts + 16 * (q + 1), sr[(q + 1) & 1]);
                 } else {  // the last read of the buffer
                     tc_fence_before();
                     __syncwarp();
@@ -212,8 +218,8 @@ __global__ void __launch_bounds__(kwt::NT, 1)
                 }
                 const uint32_t* x = sr[q & 1];
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(lb + 32 * q + c);
+                for (int c = 0; c < 16; c += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(lb + 16 * q + c);
                     const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc,
                                                  make_float2(l4.x, l4.y));
                     const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc,
@@ -221,10 +227,10 @@ __global__ void __launch_bounds__(kwt::NT, 1)
                     float2 e0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
                     float2 e1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
                     if constexpr (MASK) {
-                        if (32 * q + c < first) e0.x = 0.f;
-                        if (32 * q + c + 1 < first) e0.y = 0.f;
-                        if (32 * q + c + 2 < first) e1.x = 0.f;
-                        if (32 * q + c + 3 < first) e1.y = 0.f;
+                        if (16 * q + c < first) e0.x = 0.f;
+                        if (16 * q + c + 1 < first) e0.y = 0.f;
+                        if (16 * q + c + 2 < first) e1.x = 0.f;
+                        if (16 * q + c + 3 < first) e1.y = 0.f;
                     }
                     acc[0] = __fadd2_rn(acc[0], e0);
                     acc[1] = __fadd2_rn(acc[1], e1);
@@ -234,9 +240,10 @@ __global__ void __launch_bounds__(kwt::NT, 1)
         bool ok = true;
         for (int i = grp, turn = 0; i < n_mine; i += NG, ++turn) {
             float* lb = ls + (turn & 1) * TQ;
-            lb[r] = -next;
-            named_barrier(1 + grp, 128);
-            next = lse_of(i + NG);
+#pragma unroll
+            for (int k = 0; k < TQ / 32; ++k) lb[32 * k + lane] = next[k] == -INFINITY ? -INFINITY : -next[k] * kLog2e;
+            __syncwarp();
+            fetch(i + NG);
             const int buf = i % NBUF;
             if (ok) ok = mbar_wait(smem_u32(&s_ready[buf]), (i / NBUF) & 1, p.status);
             tc_fence_after();
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(kwt::NT, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == W_LOAD) tmem_dealloc(tmem, 512);
+    if (warp == W_LOAD) tmem_dealloc(tmem, NBUF * TQ);
     if (cluster > 1) cluster_sync();
     if (rank == 0 && threadIdx.x < TK) {
         const int key = j0 + threadIdx.x;
