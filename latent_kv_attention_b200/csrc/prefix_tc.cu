@@ -82,39 +82,58 @@ __global__ void __launch_bounds__(ptc::NT, 1)
     if (kend <= kbeg) return;
     const int n_kt = cdiv(kend - kbeg, TK), nb = cdiv(kend - kbeg, TB);  // tiles of keys, blocks of scores
 
-    if (threadIdx.x == 0) {
-        s_abort = 0;
-        mbar_init(smem_u32(q_full), 1);
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), n_qt);
-        }
-        for (int i = 0; i < 2; ++i) {
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(smem_u32(&s_ready[2 * i + h]), 1);
-                mbar_init(smem_u32(&p_ready[2 * i + h]), 4);
-                mbar_init(smem_u32(&o_ready[2 * i + h]), 1);
+    // The loader sets up the barriers and issues what needs no waiting before the block meets: Q, then K_0, V_0, K_1, ...
+    // as far as the ring goes.  One lane per box of a tile (a tile is one box, or one per page piece); the rows of tile
+    // j + 1 are looked up while its ring stage is still in use, once for its keys and values.
+    const uint32_t qb = smem_u32(q_full);
+    const int box_r = lane * g.box_rows;
+    int y = 0, z = kvh, issued = 0;
+    auto look_up = [&](int j) {
+        const int tok = kbeg + j * TK + box_r;
+        if (box_r >= TK) return;
+        y = tok;
+        if (p.ptable) {
+            // pages [num_pages][h_kv][page_size]; rows past the keys of this split are not looked up
+            int page = tok < kend ? p.ptable[tok / p.page_size] : 0;
+            if (page < 0 || page >= p.num_pages) {
+                atomicOr(p.status, kDevBadPage);
+                page = 0;
             }
-            mbar_init(smem_u32(&o_done[i]), 1);
+            y = tok % p.page_size;
+            z = page * p.h_kv + kvh;
         }
-        mbar_init(smem_u32(v_tail), 1);
-        fence_barrier_init();
-    }
+    };
+    auto issue_tile = [&]() {
+        const int s = issued % C::NS;
+        const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + C::OFF_RING + s * C::TILE) + box_r * 128;
+        if (lane == 0) mbar_arrive_expect_tx(fb, C::TILE);
+        __syncwarp();
+        if (box_r < TK) {
+            const CUtensorMap* map = issued & 1 ? &tm_v : &tm_k;
+#pragma unroll
+            for (int x = 0; x < C::NB; ++x) tma_load_3d(dst + x * C::BOX, map, x * 64, y, z, fb);
+        }
+        if (issued & 1) look_up(issued / 2 + 1);
+        ++issued;
+    };
     if (warp == W_LOAD) {
-        tmem_alloc(tmem_slot, C::T_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-
-    if (warp == W_LOAD) {
-        // ------------------------------ producer: Q, then K_0, V_0, K_1, V_1, ... ------------------------------
-        // One lane per box of a tile (a tile is one box, or one per page piece); the rows of tile j + 1 are looked up
-        // while its ring stage is still in use, once for its keys and values.
-        const uint32_t qb = smem_u32(q_full);
         if (lane == 0) {
+            s_abort = 0;
+            mbar_init(smem_u32(q_full), 1);
+            for (int s = 0; s < C::NS; ++s) {
+                mbar_init(smem_u32(&full[s]), 1);
+                mbar_init(smem_u32(&empty[s]), n_qt);
+            }
+            for (int i = 0; i < 2; ++i) {
+                for (int h = 0; h < 2; ++h) {
+                    mbar_init(smem_u32(&s_ready[2 * i + h]), 1);
+                    mbar_init(smem_u32(&p_ready[2 * i + h]), 4);
+                    mbar_init(smem_u32(&o_ready[2 * i + h]), 1);
+                }
+                mbar_init(smem_u32(&o_done[i]), 1);
+            }
+            mbar_init(smem_u32(v_tail), 1);
+            fence_barrier_init();
             mbar_arrive_expect_tx(qb, n_qt * C::NB * g.rows * 128);
             for (int i = 0; i < n_qt; ++i) {
                 const int t = 2 * pair + i;
@@ -124,40 +143,25 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                     tma_load_4d(smem_u32(smem + i * C::TILE + x * C::BOX), &tm_q, x * 64, g0, kvh, b0, qb);
             }
         }
-        const int r = lane * g.box_rows;
-        int y = 0, z = kvh;
-        auto look_up = [&](int j) {
-            const int tok = kbeg + j * TK + r;
-            if (r >= TK) return;
-            y = tok;
-            if (p.ptable) {
-                // pages [num_pages][h_kv][page_size]; rows past the keys of this split are not looked up
-                int page = tok < kend ? p.ptable[tok / p.page_size] : 0;
-                if (page < 0 || page >= p.num_pages) {
-                    atomicOr(p.status, kDevBadPage);
-                    page = 0;
-                }
-                y = tok % p.page_size;
-                z = page * p.h_kv + kvh;
-            }
-        };
+        __syncwarp();
         look_up(0);
-        int issued = 0;
+        while (issued < min(C::NS, 2 * n_kt)) issue_tile();
+    } else if (warp == W_MMA) {
+        tmem_alloc(tmem_slot, C::T_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == W_LOAD) {
+        // ------------------------------ loader ------------------------------
         bool ok = true;
-        for (int n = 0; n < 2 * n_kt; ++n) {
-            const int s = n % C::NS;
-            if (n >= C::NS) ok = mbar_wait(smem_u32(&empty[s]), (n / C::NS - 1) & 1, p.status);
+        while (issued < 2 * n_kt) {
+            ok = mbar_wait(smem_u32(&empty[issued % C::NS]), (issued / C::NS - 1) & 1, p.status);
             if (!__all_sync(0xffffffffu, ok && !*(volatile int*)&s_abort)) break;
-            const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + C::OFF_RING + s * C::TILE) + r * 128;
-            if (lane == 0) mbar_arrive_expect_tx(fb, C::TILE);
-            __syncwarp();
-            if (r < TK) {
-                const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
-#pragma unroll
-                for (int x = 0; x < C::NB; ++x) tma_load_3d(dst + x * C::BOX, map, x * 64, y, z, fb);
-            }
-            ++issued;
-            if (n & 1) look_up(n / 2 + 1);
+            issue_tile();
         }
         if (!ok) s_abort = 1;
         // every issued copy lands before the CTA may end
@@ -331,27 +335,41 @@ __global__ void __launch_bounds__(ptc::NT, 1)
         const int t = 2 * pair + i;
         const int b = g.per_seq > 1 ? t / g.per_seq : t * g.seqs + r / p.R, gr = g.per_seq > 1 ? t % g.per_seq * g.rows + r : r % p.R;
         const bool mine = ok && r < g.rows && b < p.B && gr < p.R;
-        const size_t at = mine ? (((size_t)b * p.h_kv + kvh) * p.R + gr) * p.n_slots + split : 0;
+        const long long at = mine ? (long long)((((size_t)b * p.h_kv + kvh) * p.R + gr) * p.n_slots + split) : -1;
         const float l = l2.x + l2.y, inv = l > 0.f ? 1.f / l : 0.f;
-        float* po = p.part_o + at * D;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + c, o);
-            tmem_ld_wait();
-            if (mine) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4*>(po + c + e) =
-                        make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                    __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            }
-        }
         if (mine) p.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+        // O leaves through this warp's quarter of the row tile's query buffer (its products are done), half of the
+        // columns at a time: rows written by their lanes in 16-byte chunks, permuted over the banks, and read back row
+        // by row (a lane writing its own row of the result touches 32 rows per instruction: 12,000 cycles per CTA)
+        constexpr int NC = D / 8;  // chunks of half a row
+        uint8_t* buf = smem + i * C::TILE + (warp % 4) * (32 * NC * 16);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + half * (D / 2) + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<float4*>(buf + lane * (NC * 16) + (((c / 4 + e) ^ (lane % NC)) * 16)) =
+                        make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                    __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += 32 / NC) {
+                const int rr = r0 + lane / NC, c = lane % NC;
+                const long long to_row = __shfl_sync(0xffffffffu, at, rr);
+                const float4 v = *reinterpret_cast<const float4*>(buf + rr * (NC * 16) + ((c ^ (rr % NC)) * 16));
+                if (to_row >= 0) *reinterpret_cast<float4*>(p.part_o + to_row * D + half * (D / 2) + c * 4) = v;
+            }
+            __syncwarp();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == W_LOAD) tmem_dealloc(tmem, C::T_COLS);
+    if (warp == W_MMA) tmem_dealloc(tmem, C::T_COLS);
 }
 
 PrefixTiles prefix_tiles(int B, int R) {
