@@ -296,9 +296,15 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
                           static_cast<const __nv_bfloat16*>(p.q) + global_row(p, *w, lane) * D, D * 2, qb);
             ++item;
         };
-        for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+        // Items are handed out as blocks get to them (their lengths differ); the next number is asked for an item ahead.
+        auto ask = [&]() { return lane == 0 ? (int)gridDim.x + atomicAdd(p.next_item, 1) : 0; };
+        int asked = ask();
+        for (int idx = blockIdx.x; ok && idx < n_items;) {
+            const int mine = idx;
+            idx = __shfl_sync(0xffffffffu, asked, 0);
+            if (idx < n_items) asked = ask();
             Work w;
-            if (!find_work(p, C::ROWS, idx, w, lane == 0)) continue;
+            if (!find_work(p, C::ROWS, mine, w, lane == 0)) continue;
             next_item(&w);
             const CUtensorMap* mk = w.prefix ? &tm_kp : &tm_k;
             const CUtensorMap* mv = w.prefix ? &tm_vp : &tm_v;
@@ -687,6 +693,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
     const int seen = p.causal ? L - p.s + t + 1 : L;
     const int np = cdiv(P, p.pre_tokens), n = np + cdiv(seen, p.suf_tokens), gap = p.n_pre - np;
     pdl_wait();
+    if (row == 0 && lane == 0) *p.next_item = 0;  // for the next call
     const float* pl = p.part_lse + row * p.n_slots;
     float x[kMaxSlots / 32], M = -INFINITY;
 #pragma unroll
@@ -917,6 +924,7 @@ lka_status_t prefix_run(PrefixParams& p, int d, float scale, lka_dtype_t dtype, 
     if (!aligned16(ws)) return LKA_ERR_INVALID_ARG;
     uint8_t* w = static_cast<uint8_t*>(ws);
     p.status = reinterpret_cast<uint32_t*>(w);
+    p.next_item = reinterpret_cast<int*>(w + 64);  // in the status header, which is 0 when the workspace is new
     p.part_lse = reinterpret_cast<float*>(w + pl.off_lse);
     p.part_o = reinterpret_cast<float*>(w + pl.off_o);
     p.ratio = p.h_q / p.h_kv;

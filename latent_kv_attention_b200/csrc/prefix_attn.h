@@ -17,6 +17,7 @@ struct PrefixParams {
     float* lse;                  // [B, h_q, s] natural log, or null
     float *part_o, *part_lse;    // [B * h_q * s][n_slots][D] and [..][n_slots] (log2 domain)
     uint32_t* status;
+    int* next_item;              // items handed out beyond the first of every block; 0 between calls
     int B, h_q, h_kv, s, ratio, R, Lp, Lmax, causal;
     int pre_tokens, n_pre, suf_tokens, n_suf, n_slots;
     int do_prefix, do_suffix;    // which items a launch holds
