@@ -299,12 +299,12 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
         // Items are handed out as blocks get to them (their lengths differ); the next number is asked for an item ahead.
         auto ask = [&]() { return lane == 0 ? (int)gridDim.x + atomicAdd(p.next_item, 1) : 0; };
         int asked = ask();
-        for (int idx = blockIdx.x; ok && idx < n_items;) {
-            const int mine = idx;
-            idx = __shfl_sync(0xffffffffu, asked, 0);
-            if (idx < n_items) asked = ask();
+        for (int idx = blockIdx.x, next; ok && idx < n_items; idx = next) {
             Work w;
-            if (!find_work(p, C::ROWS, mine, w, lane == 0)) continue;
+            const bool some = find_work(p, C::ROWS, idx, w, lane == 0);
+            next = __shfl_sync(0xffffffffu, asked, 0);
+            if (next < n_items) asked = ask();
+            if (!some) continue;
             next_item(&w);
             const CUtensorMap* mk = w.prefix ? &tm_kp : &tm_k;
             const CUtensorMap* mv = w.prefix ? &tm_vp : &tm_v;
@@ -756,14 +756,13 @@ struct PrefixPlan {
 
 // Keys per split of `units` row blocks over L keys: the split count n <= 64 that minimises waves x (tiles per split
 // + 2), the 2 for a block's start and end, where the waves of w = units n / slots cost max(ceil(w), w + 1/4).
-// `ragged` lengths leave an average tail beyond the mean; equal ones end together and cost ceil(w) waves.
-int split_keys(double units, double slots, int L, int tile, bool ragged = true) {
+int split_keys(double units, double slots, int L, int tile) {
     const int lt = cdiv(std::max(L, 1), tile);
     int best = 1;
     double best_cost = -1.0;
     for (int n = 1; n <= lt && n <= kMaxSplits; ++n) {
         const double w = units * n / slots;
-        const double cost = fmax(ceil(w - 1e-9), ragged ? w + 0.25 : w) * (cdiv(lt, n) + 2);
+        const double cost = fmax(ceil(w - 1e-9), w + 0.25) * (cdiv(lt, n) + 2);
         if (best_cost < 0.0 || cost < best_cost - 1e-9) {
             best_cost = cost;
             best = n;
@@ -789,6 +788,28 @@ int stream_keys(double units, double slots, int L, int tile) {
     return cdiv(lt, best) * tile;
 }
 
+// Keys per split of the tensor-core prefix kernel, planned with the suffix kernel that shares the SMs with it: blocks of
+// the suffix kernel run where prefix blocks leave an SM free, and everywhere once they are done.  In units of a key
+// tile's time in a prefix block (1.85 us): a block costs its tiles + 2.7, a 64-key suffix tile 0.4 d / 128 of an SM, a
+// suffix block 2 to start; suffixes count at half their capacity.  (64 sequences over a prefix of 8192: 8 splits, half
+// the SMs, instead of 16.)
+int tc_keys(int pairs_heads, int Lp, double suffix_tiles, int d) {
+    const int lt = cdiv(std::max(Lp, 1), 128), sms = sm_count();
+    const double suffix = 0.5 * suffix_tiles * 0.4 * d / 128;
+    int best = 1;
+    double best_cost = -1.0;
+    for (int n = 1; n <= lt && n <= kMaxSplits; ++n) {
+        const double blocks = (double)pairs_heads * n, waves = ceil(blocks / sms), t = waves * (cdiv(lt, n) + 2.7);
+        const double free_sms = sms - blocks / waves, left = suffix - free_sms * fmax(t - 2.0, 0.0);
+        const double cost = t + (left > 0.0 ? 2.0 + left / sms : 0.0);
+        if (best_cost < 0.0 || cost < best_cost - 1e-9) {
+            best_cost = cost;
+            best = n;
+        }
+    }
+    return cdiv(lt, best) * 128;
+}
+
 lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lmax, lka_dtype_t dtype, PrefixPlan* pl) {
     if (B < 0 || h_q < 1 || h_kv < 1 || s < 1 || d < 1 || Lp < 0 || Lmax < 1 || h_q % h_kv) return LKA_ERR_INVALID_ARG;
     if (dtype != LKA_BF16 && dtype != LKA_FP32) return LKA_ERR_UNSUPPORTED;
@@ -809,7 +830,8 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     auto by_knob = [knob](int L, int unit) { return cdiv(std::max(knob, cdiv(L, kMaxSplits)), unit) * unit; };
     if (pl->tc)
         pl->pre_tokens = knob > 0 ? by_knob(Lp, 128)
-                                  : split_keys((double)h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), sm_count(), Lp, 128, false);
+                                  : tc_keys(h_kv * cdiv(prefix_tiles(Bn, R).n_tiles, 2), Lp,
+                                            (double)Bn * h_kv * cdiv(R, 16) * cdiv(Lmax, 64), d);
     else
         pl->pre_tokens = knob > 0 ? by_knob(Lp, tile)
                                   : f32 || rows64 ? split_keys((double)h_kv * cdiv(Bn * R, pl->rows_pre), slots, Lp, tile)
