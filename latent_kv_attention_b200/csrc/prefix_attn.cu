@@ -223,8 +223,9 @@ struct StreamCfg {
     static constexpr int NS = D == 64 ? 4 : 3;
     static constexpr int BLOCKS = D == 64 ? 3 : D == 128 ? 2 : 1;          // per SM
     static constexpr int QROW = D * 2 + 16;                                // padded: ldmatrix without bank conflicts
-    static constexpr int OFF_Q = NS * STAGE, OFF_O = OFF_Q + ROWS * QROW;  // O: [16][D] fp32, the join
-    static constexpr int OFF_ML = OFF_O + ROWS * D * 4;                    // [4][16] maxima, then sums
+    static constexpr int OROW = D + 8;                                     // fp32 values, padded likewise
+    static constexpr int OFF_Q = NS * STAGE, OFF_O = OFF_Q + ROWS * QROW;  // O: [16][OROW], the join
+    static constexpr int OFF_ML = OFF_O + ROWS * OROW * 4;                 // [4][16] maxima, then sums
     static constexpr int OFF_BAR = OFF_ML + 2 * 4 * ROWS * 4;
     static constexpr int SMEM = 1024 + OFF_BAR + 128;
     static_assert((SMEM + 1024) * BLOCKS <= 233472, "shared memory");
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
                     if (r >= w.nrows) continue;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
-                        float2* x = reinterpret_cast<float2*>(om + r * D + i * 8 + 2 * t);
+                        float2* x = reinterpret_cast<float2*>(om + r * C::OROW + i * 8 + 2 * t);
                         float2 v = make_float2(st.o[i][2 * h] * f[h], st.o[i][2 * h + 1] * f[h]);
                         if (k) v = __fadd2_rn(v, *x);
                         *x = v;
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
 #pragma unroll
             for (int k = 0; k < 4; ++k) sum += M == -INFINITY ? 0.f : fast_exp2(ml[k * 16 + r] - M) * ml[64 + k * 16 + r];
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const float4 x = *reinterpret_cast<const float4*>(om + r * D + c * 4);
+            const float4 x = *reinterpret_cast<const float4*>(om + r * C::OROW + c * 4);
             const size_t to = global_row(p, w, r) * p.n_slots + w.slot;
             *reinterpret_cast<float4*>(p.part_o + to * D + c * 4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
             if (c == 0) p.part_lse[to] = sum > 0.f ? M + log2f(sum) : -INFINITY;
@@ -678,14 +679,16 @@ __global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
 }
 
 // ---- the merge ---------------------------------------------------------------------------------------------------
-// One warp per row.  A row's parts are the prefix splits its length reaches and the suffix splits with a key that the
-// row sees; the lanes fetch their lse together, then every lane joins its D / 32 values, eight parts in flight.
-template <typename T, int D>
+// WPR warps per row (four where there are few rows and many parts to a row, one otherwise).  A row's parts are the
+// prefix splits its length reaches and the suffix splits with a key that the row sees; the lanes fetch their lse
+// together, then every warp joins its share of the parts, every lane D / 32 values, eight parts in flight.
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p) {
     constexpr int VPL = D / 32;
     __shared__ float fs[4][kMaxSlots];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const size_t row = (size_t)blockIdx.x * 4 + warp;
+    __shared__ __align__(16) float others[WPR > 1 ? 3 : 1][WPR > 1 ? D : 4];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = warp % WPR;
+    const size_t row = (size_t)blockIdx.x * (4 / WPR) + warp / WPR;
     if (row >= (size_t)p.B * p.h_q * p.s) return;
     const int b = (int)(row / ((size_t)p.h_q * p.s)), t = (int)(row % p.s);
     const int P = prefix_length(p, false);
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
     const int seen = p.causal ? L - p.s + t + 1 : L;
     const int np = cdiv(P, p.pre_tokens), n = np + cdiv(seen, p.suf_tokens), gap = p.n_pre - np;
     pdl_wait();
-    if (row == 0 && lane == 0) *p.next_item = 0;  // for the next call
+    if (row == 0 && threadIdx.x == 0) *p.next_item = 0;  // for the next call
     const float* pl = p.part_lse + row * p.n_slots;
     float x[kMaxSlots / 32], M = -INFINITY;
 #pragma unroll
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
     const float* po = p.part_o + row * p.n_slots * D + lane * VPL;
     float a[VPL] = {};
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) {
+    for (int i = share; i < n; i += WPR) {
         const float f = fs[warp][i];
         const float* src = po + (size_t)(i < np ? i : i + gap) * D;
         float y[VPL];
@@ -729,6 +732,18 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
         }
 #pragma unroll
         for (int e = 0; e < VPL; ++e) a[e] = fmaf(f, y[e], a[e]);
+    }
+    if constexpr (WPR > 1) {
+        if (share > 0) {
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) others[share - 1][lane * VPL + e] = a[e];
+        }
+        __syncthreads();
+        if (share > 0) return;
+#pragma unroll
+        for (int k = 0; k < WPR - 1; ++k)
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) a[e] += others[k][lane * VPL + e];
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(p.out) + row * D + lane * VPL;
@@ -744,6 +759,14 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
         for (int e = 0; e < VPL; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
     }
     if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+template <typename T, int D>
+cudaError_t launch_merge(const PrefixParams& p, cudaStream_t st) {
+    const size_t rows = (size_t)p.B * p.h_q * p.s;
+    if (p.n_slots > 8 && rows <= 4u * sm_count())
+        return launch_pdl<prefix_merge_kernel<T, D, 4>>(dim3((unsigned)rows), 128, 0, st, p);
+    return launch_pdl<prefix_merge_kernel<T, D, 1>>(dim3((unsigned)((rows + 3) / 4)), 128, 0, st, p);
 }
 
 // ---- planning ------------------------------------------------------------------------------------------------------
@@ -915,8 +938,7 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
     }
     if (e == cudaSuccess) e = launch_stream<D>(p, st);
     if (e != cudaSuccess) return e;
-    const size_t rows = (size_t)p.B * p.h_q * p.s;
-    return launch_pdl<prefix_merge_kernel<__nv_bfloat16, D>>(dim3((unsigned)((rows + 3) / 4)), 128, 0, st, p);
+    return launch_merge<__nv_bfloat16, D>(p, st);
 }
 
 template <int D>
@@ -925,8 +947,7 @@ cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
     const cudaError_t e = launch_items<prefix_f32_kernel<D>>(F32Cfg<D>::SMEM, p, 16, st);
     timer.stop();
     if (e != cudaSuccess) return e;
-    const size_t rows = (size_t)p.B * p.h_q * p.s;
-    return launch_pdl<prefix_merge_kernel<float, D>>(dim3((unsigned)((rows + 3) / 4)), 128, 0, st, p);
+    return launch_merge<float, D>(p, st);
 }
 
 lka_status_t prefix_run(PrefixParams& p, int d, float scale, lka_dtype_t dtype, void* ws, size_t ws_bytes,
