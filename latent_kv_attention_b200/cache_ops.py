@@ -23,6 +23,7 @@ _E4M3 = torch.float8_e4m3fn
 _Tensor = torch.Tensor
 _CACHE_DT = {torch.bfloat16: 0, torch.float32: 1, _E4M3: 2}
 _HEADER = 256  # bytes of a workspace that hold the status word
+_TOO_SMALL = 3  # LKA_ERR_WORKSPACE
 
 _captured = {}
 _captured_lock = threading.Lock()
@@ -102,28 +103,30 @@ def _function(name):
     return f
 
 
-def _call(name, device, args, scratch=_HEADER):
-    """Calls the library on the device's current stream, with a workspace of `scratch` bytes after `args` (none if
-    scratch is 0).  A captured call gets its scratch from the graph's memory."""
+def _call(name, device, args, sizes=None):
+    """Calls the library on the device's current stream, with a workspace after `args`: the stream's own, of the status
+    header alone or, with `sizes` (the arguments of the matching *_workspace_size), of what the call needs.  A captured
+    call gets its scratch from the graph's memory."""
     index = device.index
     if _device_now() != index:
         with torch.cuda.device(device):
-            return _call(name, device, args, scratch)
+            return _call(name, device, args, sizes)
     f, stream = _function(name), _stream_now(index)
-    if scratch == 0:
-        rc = f(*args, stream)
-    elif not _capturing():
+    if not _capturing():
         if index not in _captured:
             captured_status(device, create=True)  # outside a graph, so that no replay clears it
         ws = workspaces._ws.get((index, stream))
-        if ws is None or ws.numel() < scratch:
-            ws = workspaces.get(scratch, device)
+        if ws is None:
+            ws = workspaces.get(_HEADER, device)
         rc = f(*args, ws.data_ptr(), ws.numel(), stream)
-    elif scratch <= _HEADER:
+        if rc == _TOO_SMALL and sizes is not None:  # nothing was enqueued
+            ws = workspaces.get(_function(name + "_workspace_size")(*sizes), device)
+            rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+    elif sizes is None:
         ws = captured_status(device, create=True)
         rc = f(*args, ws.data_ptr(), ws.numel(), stream)
     else:
-        ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+        ws = torch.empty(max(_function(name + "_workspace_size")(*sizes), _HEADER), dtype=torch.uint8, device=device)
         ws[:_HEADER].zero_()
         rc = f(*args, ws.data_ptr(), ws.numel(), stream)
         # the captured call's flags outlive its scratch
@@ -187,9 +190,15 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
         _require(at >= x.data_ptr() + span * e or x.data_ptr() >= at + out.numel() * e,
                  "out must be x itself or share no memory with it")
     os = out.stride()
-    _call("rope_apply", dev, (x.data_ptr(), _I3(xs[0], xs[1], xs[2]), pos, freq, out.data_ptr(),
-                              _I3(os[0], os[1], os[2]), B, h, s, d, 2 * inv_freq.numel(), bool(interleaved),
-                              bool(backward), amplitude, code), scratch=0)
+    args = (x.data_ptr(), _I3(xs[0], xs[1], xs[2]), pos, freq, out.data_ptr(), _I3(os[0], os[1], os[2]), B, h, s, d,
+            2 * inv_freq.numel(), bool(interleaved), bool(backward), amplitude, code)
+    if _device_now() == dev.index:
+        rc = _function("rope_apply")(*args, _stream_now(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = _function("rope_apply")(*args, _stream_now(dev.index))
+    if rc:
+        _check("rope_apply", rc)
     return out
 
 
@@ -369,9 +378,9 @@ def gqa_attn_shared_prefix(q, k_prefix, v_prefix, k, v, cache_lens, prefix_len=N
     ko, vo = _dense(k, "k", dt, dev, own), _dense(v, "v", dt, dev, own)
     lens, plen = _lens(cache_lens, B, dev), _prefix_len(prefix_len, dev)
     out, lse, lp = _attn_outputs(q, out, return_lse)
-    n = _function("gqa_attn_shared_prefix_workspace_size")(B, h_q, h_kv, s, d, Lp, Lmax, code)
     _call("gqa_attn_shared_prefix", dev, (qp, kp, vp, plen, ko, vo, lens, out.data_ptr(), lp, B, h_q, h_kv, s, d, Lp,
-                                          Lmax, bool(causal), _scale(scale, d), code), max(n, _HEADER))
+                                          Lmax, bool(causal), _scale(scale, d), code),
+          (B, h_q, h_kv, s, d, Lp, Lmax, code))
     return (out, lse) if return_lse else out
 
 
@@ -393,10 +402,10 @@ def gqa_attn_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, 
     mp, (table, max_pages) = prefix_table.shape[0], _table(block_table, B, dev)
     lens, plen = _lens(cache_lens, B, dev), _prefix_len(prefix_len, dev)
     out, lse, lp = _attn_outputs(q, out, return_lse)
-    n = _function("gqa_attn_shared_prefix_paged_workspace_size")(B, h_q, h_kv, s, d, page_size, mp, max_pages, code)
     _call("gqa_attn_shared_prefix_paged", dev, (qp, kp, vp, ptab, plen, table, lens, out.data_ptr(), lp, B, h_q, h_kv,
                                                 s, d, page_size, mp, max_pages, num_pages, bool(causal),
-                                                _scale(scale, d), code), max(n, _HEADER))
+                                                _scale(scale, d), code),
+          (B, h_q, h_kv, s, d, page_size, mp, max_pages, code))
     return (out, lse) if return_lse else out
 
 
