@@ -95,6 +95,37 @@ def gta_flops(lens: Sequence[int], G: int, H: int, d_qk: int, d_v: int, s_q: int
     return sum(_visible(int(L), s_q, causal) for L in lens) * (G * 2 * d_qk + H * 2 * d_v)
 
 
+# ---- the operators around the attention calls (cache_ops) -------------------------------------------------------
+def rope_append_bytes(tokens: int, h_q: int, h_kv: int, d: int, elem: int = 2, cache_elem: int | None = None) -> int:
+    """q, k, v read once, the rotated queries and the cache rows written once."""
+    cache_elem = elem if cache_elem is None else cache_elem
+    return tokens * d * (2 * h_q * elem + 2 * h_kv * (elem + cache_elem))
+
+
+def shared_prefix_bytes(prefix: int, lens: Sequence[int], h_q: int, h_kv: int, d: int, s_q: int, elem: int = 2) -> int:
+    """The prefix's cache read once for the whole batch, every suffix's once, q read and out written."""
+    return (prefix + sum(int(L) for L in lens)) * h_kv * 2 * d * elem + len(lens) * h_q * s_q * d * elem * 2
+
+
+def shared_prefix_flops(prefix: int, lens: Sequence[int], h_q: int, d: int, s_q: int, causal: bool) -> int:
+    return gqa_flops(lens, h_q, d, s_q, causal) + prefix * len(lens) * s_q * h_q * 4 * d
+
+
+def key_weights_bytes(lens: Sequence[int], h_q: int, h_kv: int, d: int, s_q: int, Lmax: int, elem: int = 2) -> int:
+    """Keys, queries and normalisers read once, one fp32 weight per cache slot written."""
+    return (sum(int(L) for L in lens) * h_kv * d * elem + len(lens) * h_q * s_q * (d * elem + 4) +
+            len(lens) * h_kv * Lmax * 4)
+
+
+def key_weights_flops(lens: Sequence[int], h_q: int, d: int, s_q: int, causal: bool) -> int:
+    return sum(_visible(int(L), s_q, causal) for L in lens) * h_q * 2 * d
+
+
+def evict_bytes(lens: Sequence[int], h_kv: int, d: int, budget: int, elem: int = 2) -> int:
+    """Every weight read once, the kept rows of K, V and the weights read and written, the list of positions written."""
+    return sum(h_kv * (4 * int(L) + min(int(L), budget) * (4 * d * elem + 4) + 4 * budget) for L in lens)
+
+
 def arithmetic_intensity_per_token(h_q: int, qk_dims: int, v_dims: int, cache_elems: int, s_q: int = 1,
                                    elem: int = 2) -> float:
     """FLOPs per cache byte of one decode step, counted per cached token (s_q query tokens)."""

@@ -218,3 +218,17 @@ def test_binding_refuses_cpu_tensors():
         lka.gqa_evict(x, x, torch.zeros(1, 2, 3), lens, 0)
     with pytest.raises(ValueError):
         lka.rope(x.half(), torch.zeros(1, 3, dtype=torch.int32), f)
+
+
+# ------------------------------------------------------------------ byte and FLOP counts
+def test_costs_against_counting():
+    from latent_kv_attention_b200 import costs
+
+    assert costs.rope_append_bytes(3, 8, 2, 64) == 3 * 64 * 2 * (8 + 8 + 2 + 2 + 2 + 2)
+    assert costs.rope_append_bytes(1, 8, 2, 64, 2, 1) == 64 * (8 * 4 + 2 * 6)
+    # 2 sequences of suffix 3 and 5 over a prefix of 10, two causal queries each: 10 + 2 and 10 + 3, 10 + 4 and 10 + 5 keys
+    assert costs.shared_prefix_flops(10, [3, 5], 4, 64, 2, True) == (12 + 13 + 14 + 15) * 4 * 4 * 64
+    assert costs.shared_prefix_bytes(10, [3, 5], 4, 2, 64, 2) == 18 * 2 * 2 * 64 * 2 + 2 * 4 * 2 * 64 * 2 * 2
+    assert costs.key_weights_flops([3, 5], 4, 64, 2, True) == (2 + 3 + 4 + 5) * 4 * 2 * 64
+    assert costs.key_weights_bytes([3, 5], 4, 2, 64, 2, 8) == 8 * 2 * 64 * 2 + 2 * 4 * 2 * (128 + 4) + 2 * 2 * 8 * 4
+    assert costs.evict_bytes([3, 9], 2, 64, 4) == 2 * (12 + 3 * 516 + 16) + 2 * (36 + 4 * 516 + 16)

@@ -396,6 +396,23 @@ def test_prefix_equals_gqa_attn_over_the_joined_cache():
     assert_lse_close(lse, ref_lse, torch.bfloat16, "joined lse")
 
 
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 0.5])
+@pytest.mark.parametrize("B,d,dtype", [(3, 128, "bf16"), (40, 64, "bf16"), (40, 128, "bf16"), (12, 256, "bf16"), (3, 64, "fp32")])
+def test_prefix_scales_and_growing_scores(B, d, dtype, scale):
+    """Scores that grow along the keys move the reference maximum again and again; negative and zero scales turn and
+    flatten them."""
+    case = (B, 8, 2, 1, d, 900, 100, True, dtype, 0)
+    q, kp, vp, k, v, lens, n, dt = prefix_case(case, 90 + B)
+    if scale > 0:  # up to about e^30 from the first key to the last
+        kp *= torch.linspace(0.2, 4.0 / d ** 0.5 * 4, 900, device=DEV).view(1, -1, 1).to(dt)
+    out, lse = lka.gqa_attn_shared_prefix(q, kp, vp, k, v, lens, scale=scale, return_lse=True)
+    fix = scale * math.sqrt(d)  # attend() divides by sqrt(d)
+    for b, L in enumerate(lens.tolist()):
+        ref, ref_lse = attend(q[b].double() * fix, torch.cat((kp, k[b, :, :L]), 1), torch.cat((vp, v[b, :, :L]), 1), n, True)
+        assert_close(out[b], ref, dt, f"sequence {b}")
+        assert_lse_close(lse[b], ref_lse, dt, f"lse {b}")
+
+
 def test_prefix_reports_bad_lengths_and_pages():
     case = (4, 8, 2, 1, 128, 100, 30, True, "bf16", 0)
     q, kp, vp, k, v, lens, n, dt = prefix_case(case, 60)
@@ -473,6 +490,19 @@ def test_weights_of_a_causal_prompt_sum_to_its_rows():
     w = lka.gqa_key_weights(q, k, lse, lens)
     # 2400 rows; lse from bf16-probability sums is fp32-accurate: relative 1e-5 as above
     assert torch.allclose(w.double().sum(-1), torch.full((1, 2), 2400.0, dtype=torch.float64, device=DEV), rtol=1e-5)
+
+
+@pytest.mark.parametrize("s,dtype", [(1, "bf16"), (130, "bf16"), (3, "fp32")])
+@pytest.mark.parametrize("scale", [-0.07, 0.0])
+def test_weights_of_other_scales(s, dtype, scale):
+    g = gen(13)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v = (randn(g, 2, h, n, 64, dtype=dt) for h, n in ((8, s), (2, 200), (2, 200)))
+    lens = ints(200, 150)
+    _, lse = lka.gqa_attn(q, k, v, lens, scale=scale, return_lse=True)
+    ref = want_weights(q, k, lse, lens, True, scale)
+    w = lka.gqa_key_weights(q, k, lse, lens, scale=scale)
+    assert ((w - ref).abs() <= 1e-5 * ref).all()
 
 
 def test_weights_report_bad_lengths_and_pages():
