@@ -358,10 +358,18 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     if (!aligned16(ws)) return LKA_ERR_INVALID_ARG;
     p.status = static_cast<uint32_t*>(ws);
     const cudaStream_t st = (cudaStream_t)stream;
-    // Clusters while the rows alone leave SMs idle and every block has 8 weights per thread or more (with fewer, the
-    // barriers of the cluster cost more than the shorter passes save: 128 rows of 8192, 42 us alone, 47 in pairs).
+    // Up to 8192 weights a row fits one block's registers.  A longer row is shared by a cluster while all clusters run
+    // at once (whole call, 32 rows of 17,600 weights: 25 us alone, 18 in fours; 8 of 65,536: 85, 34 in fours, 23 in
+    // eights), but clusters of eight blocks of 1024 threads find few places (32 rows: 53 us), nor do fours past the
+    // number of SMs (56 rows of 17,600: 25 us alone, 31 in fours).
+    const long long rows = (long long)p.B * p.h_kv;
     int cluster = 1;
-    while (cluster < 8 && (long long)p.B * p.h_kv * cluster * 2 <= 2LL * sm_count() && p.Lmax >= 2 * kKeep * kSelThreads * cluster) cluster *= 2;
+    if (p.Lmax > 4 * kKeep * kSelThreads && rows <= 8)
+        cluster = 8;
+    else if (p.Lmax > kKeep * kSelThreads && rows * 4 <= sm_count())
+        cluster = 4;
+    else if (p.Lmax > 4 * kKeep * kSelThreads && rows * 2 <= sm_count())
+        cluster = 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.h_kv * cluster, p.B);
     cfg.blockDim = dim3(kSelThreads);

@@ -166,10 +166,11 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
     }
 }
 
-// fp32 caches: one key per lane pair (two halves of the rows), the tile and 16 query rows at a time in shared memory.
-template <int D>
+// fp32 caches: one key per lane pair (two halves of the rows), the tile and RB query rows at a time in shared memory
+// (4 where the group has no more, so that a decode step computes no empty rows).
+template <int D, int RB>
 __global__ void __launch_bounds__(128) key_weights_f32_kernel(const KeyWeightParams p) {
-    constexpr int KROW = D + 4, RB = 16;
+    constexpr int KROW = D + 4;
     extern __shared__ __align__(16) uint8_t smem[];
     float* ks = reinterpret_cast<float*>(smem);  // [kTile][KROW]
     float* qs = ks + kTile * KROW;               // [RB][D]
@@ -256,15 +257,20 @@ cudaError_t launch_mma(KeyWeightParams p, dim3 grid, cudaStream_t st) {
     return cudaPeekAtLastError();
 }
 
-template <int D>
-cudaError_t launch_f32(const KeyWeightParams& p, const dim3& grid, cudaStream_t st) {
-    constexpr int smem = (kTile * (D + 4) + 16 * D + 16 + kTile) * 4;
-    const cudaError_t e = allow_smem<key_weights_f32_kernel<D>>(smem);
+template <int D, int RB>
+cudaError_t launch_f32_rows(const KeyWeightParams& p, const dim3& grid, cudaStream_t st) {
+    constexpr int smem = (kTile * (D + 4) + RB * D + RB + kTile) * 4;
+    const cudaError_t e = allow_smem<key_weights_f32_kernel<D, RB>>(smem);
     if (e != cudaSuccess) return e;
     TimedLaunch timer(st);
-    key_weights_f32_kernel<D><<<grid, 128, smem, st>>>(p);
+    key_weights_f32_kernel<D, RB><<<grid, 128, smem, st>>>(p);
     timer.stop();
     return cudaPeekAtLastError();
+}
+
+template <int D>
+cudaError_t launch_f32(const KeyWeightParams& p, const dim3& grid, cudaStream_t st) {
+    return p.ratio * p.s <= 4 ? launch_f32_rows<D, 4>(p, grid, st) : launch_f32_rows<D, 16>(p, grid, st);
 }
 
 struct KwPages {
@@ -309,7 +315,7 @@ lka_status_t key_weights_run(const void* q, const void* k, const float* lse, con
     }
     const dim3 grid(cdiv(Lmax, kTile), h_kv, B);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == LKA_BF16 && d <= 128 && s >= kKeyWeightsTcMinQueries) return key_weights_tc(p, d, st);
+    if (dtype == LKA_BF16 && s >= kKeyWeightsTcMinQueries) return key_weights_tc(p, d, st);
     cudaError_t e;
     if (dtype == LKA_FP32)
         e = d == 64 ? launch_f32<64>(p, grid, st) : launch_f32<128>(p, grid, st);

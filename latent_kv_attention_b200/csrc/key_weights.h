@@ -23,7 +23,7 @@ struct KeyWeightParams {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Queries per head from which the tensor-core kernel runs (bf16, d = 64 and 128): a tile of 128 query rows is half
+// Queries per head from which the tensor-core kernel runs (bf16): a tile of 128 query rows is half
 // full there.
 constexpr int kKeyWeightsTcMinQueries = 64;
 lka_status_t key_weights_tc(const KeyWeightParams& p, int d, cudaStream_t st);

@@ -1,13 +1,13 @@
 // key_weights_tc.cu -- the attention weight every key received from a prompt's queries,
-// on the 5th-generation tensor cores (bf16, d = 64 and 128, many queries per head).
+// on the 5th-generation tensor cores (bf16, many queries per head).
 //
 // S^T = K Q^T: one CTA keeps a tile of 128 keys (the MMA's rows, one per tensor-memory
 // lane) and streams tiles of 128 query rows of the group's heads (the columns) through a TMA
 // ring.  A key's weight is a sum along its own lane, so nothing crosses lanes and no P is
 // written back: per score one multiply-add with the row's normaliser, one exponential, one
 // addition.  Warp 8 loads, warp 9 issues the MMAs into two score buffers of tensor memory, two
-// groups of four warps take the score tiles in turn; two CTAs per SM cover each other's starts
-// and waits.  With few key tiles, the query tiles of one key tile are dealt to the CTAs of a
+// groups of four warps take the score tiles in turn; two CTAs per SM (one at d = 256) cover
+// each other's starts and waits.  With few key tiles, the query tiles of one key tile are dealt to the CTAs of a
 // cluster, whose sums rank 0 adds in order.
 //
 // Bound: 16,384 exponentials per tile are 1024 cycles of the special-function unit (16 per
@@ -34,12 +34,13 @@ constexpr int NG = 2, W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, NT = 32 * (W_MMA + 1)
 template <int D>
 struct Cfg {
     static constexpr int NB = D / 64, BOX = 128 * 128, TILE = NB * BOX;
-    static constexpr int NS = D == 128 ? 2 : 4;  // query tiles in flight
+    static constexpr int NS = D == 64 ? 4 : 2;       // query tiles in flight
+    static constexpr int CTAS = D == 256 ? 1 : 2;    // per SM
     static constexpr int OFF_Q = TILE, OFF_LSE = OFF_Q + NS * TILE;
     static constexpr int OFF_SUM = OFF_LSE + 2 * 4 * NG * TQ * 4;  // [softmax warp][2 parities][TQ]
     static constexpr int OFF_BAR = OFF_SUM + NG * TK * 4;      // [NG][TK]
     static constexpr int SMEM = 1024 + OFF_BAR + 256;
-    static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
+    static_assert(CTAS * (SMEM + 1024) <= 233472, "shared memory");
 };
 }  // namespace kwt
 
@@ -60,7 +61,7 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kwt::NT, 2)
+__global__ void __launch_bounds__(kwt::NT, kwt::Cfg<D>::CTAS)
     key_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const KeyWeightParams p, const int cluster, const int box_rows) {
     using namespace kwt;
@@ -320,7 +321,7 @@ static lka_status_t key_weights_tc_run(const KeyWeightParams& p, cudaStream_t st
 }
 
 lka_status_t key_weights_tc(const KeyWeightParams& p, int d, cudaStream_t st) {
-    return d == 64 ? key_weights_tc_run<64>(p, st) : key_weights_tc_run<128>(p, st);
+    return d == 64 ? key_weights_tc_run<64>(p, st) : d == 128 ? key_weights_tc_run<128>(p, st) : key_weights_tc_run<256>(p, st);
 }
 
 }  // namespace lka

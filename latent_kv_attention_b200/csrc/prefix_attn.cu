@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
             *reinterpret_cast<float4*>(vs + r * D + c * 4) = y;
         }
         __syncthreads();
+        if (warp * 4 >= w.nrows) continue;  // a warp without rows only loads
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         const float* kp = ks + lane * C::KROW;
         const float* qp = qs + warp * 4 * D;

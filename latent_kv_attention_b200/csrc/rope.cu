@@ -64,7 +64,7 @@ template <typename C>
 constexpr int rope_blocks() { return sizeof(C) == 1 ? 5 : 6; }
 constexpr int kRopeBatch = 4;  // units in flight per thread
 constexpr int kRopeMaxPairs = 256;
-constexpr int kRopeMaxTokens = 8, kRopeTable = 512;  // tokens per CTA, (cos, sin) pairs of its tables
+constexpr int kRopeMaxTokens = 16, kRopeTable = 512;  // tokens per CTA, (cos, sin) pairs of its tables
 
 template <typename T, int VE>
 struct VecOf;
