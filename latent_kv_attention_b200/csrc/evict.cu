@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 // step (and the next one) before it writes.
 constexpr int kMoveThreads = 256, kMoveUnroll = 4;
 
-constexpr int kCopyUnroll = 8;  // rows a thread has in flight where nothing orders them
+constexpr int kCopyUnroll = 4;  // rows a thread has in flight where nothing orders them
 
 template <typename V, bool IN_PLACE>
 __device__ __forceinline__ void move_rows(const EvictParams& p, const uint8_t* src, uint8_t* dst, int64_t src_row0,
@@ -289,7 +289,7 @@ struct MovePlan {
 };
 
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, const MovePlan m) {
+__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 4 : 7) evict_move_kernel(const EvictParams p, const MovePlan m) {
     const int h = blockIdx.y, b = blockIdx.z;
     const int range = blockIdx.x % m.ranges, what = blockIdx.x / m.ranges;
     const int32_t* kept = p.kept + ((size_t)b * p.h_kv + h) * p.budget;
