@@ -404,6 +404,8 @@ LKA_API lka_status_t latent_rope_append_fp8kv(const void *q_r, const void *c_kv,
  *   prefix_len: device int32 [1] with 0 <= P <= Lp (clamped and reported), or NULL for P = Lp; Lp may be 0.
  * bf16 (d_h in {64, 128, 256}) or fp32 (d_h in {64, 128}).  The prefix is read once for the query rows of all
  * sequences together; softmax statistics and partial outputs are fp32.
+ * A non-finite value in a row that only some queries of the step see can reach the others, as in (a).
+ * The workspace header also holds a work counter, 0 between calls.
  * Paged: one pool for prefix and suffixes; the prefix's pages are prefix_table [max_prefix_pages], a suffix starts
  * at row 0 of its own first page block_table[b][0].  Other arguments as in (a'). */
 LKA_API size_t gqa_attn_shared_prefix_workspace_size(int B, int h_q, int h_kv, int s_q, int d_h, int Lp, int Lmax,
