@@ -342,8 +342,11 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
         if (!x || !aligned16(x)) return LKA_ERR_INVALID_ARG;
     if (p.new_lens == p.lens) return LKA_ERR_INVALID_ARG;
     const bool in_place = p.k == p.ko;
-    if (!p.table) {
+    if (p.table) {
+        if (p.ko == p.vo) return LKA_ERR_INVALID_ARG;
+    } else {
         const size_t rows_in = (size_t)p.B * p.h_kv * p.Lmax, rows_out = (size_t)p.B * p.h_kv * p.Lout;
+        if (overlap(p.ko, rows_out * p.row_bytes, p.vo, rows_out * p.row_bytes)) return LKA_ERR_INVALID_ARG;
         if (in_place) {
             if (p.v != p.vo || p.w != p.wo || p.Lmax != p.Lout) return LKA_ERR_INVALID_ARG;
         } else if (overlap(p.k, rows_in * p.row_bytes, p.ko, rows_out * p.row_bytes) ||

@@ -245,6 +245,18 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
+// Whether `pred` holds in any of the 128 consumer threads (named barrier 1 with an OR reduction).
+__device__ __forceinline__ bool any_consumer(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred)
+        : "memory");
+    return r != 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
     prefix_stream_kernel(const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
@@ -359,10 +371,8 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
     int n = 0;
     for (int item = 0;; ++item) {
         bool ok = mbar_wait(smem_u32(q_full), item & 1, p.status);
-        if (!ok || !s_more) {
-            if (!ok) s_abort = 1;
-            break;
-        }
+        if (!ok) s_abort = 1;
+        if (any_consumer(!ok || !s_more)) break;  // all or none: they meet again at the join
         const Work w = s_work;
         constexpr bool QREG = D <= 128;  // the query fragments stay in registers; otherwise they are read again per tile
         uint32_t qf[QREG ? D / 16 : 1][4];

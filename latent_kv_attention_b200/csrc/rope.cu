@@ -417,6 +417,7 @@ lka_status_t append_run(const void* q, const void* k, const void* v, const int64
     if (!strides || !elem_aligned(q, eb) || !elem_aligned(k, eb) || !elem_aligned(v, eb) || !elem_aligned(q_out, eb) ||
         !elem_aligned(c.kc, cb) || !elem_aligned(c.vc, cb) || !elem_aligned(lens, 4) || !elem_aligned(inv_freq, 8))
         return LKA_ERR_INVALID_ARG;
+    if (c.kc == c.vc) return LKA_ERR_INVALID_ARG;  // keys and values would overwrite each other
     if (positions && !elem_aligned(positions, 4)) return LKA_ERR_INVALID_ARG;
     if (c.fp8 && (!elem_aligned(c.k_scale, 4) || !elem_aligned(c.v_scale, 4))) return LKA_ERR_INVALID_ARG;
     if (!ws || ws_bytes < kWsHeaderBytes) return LKA_ERR_WORKSPACE;

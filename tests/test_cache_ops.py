@@ -18,6 +18,7 @@ def lib():
 
 P = ctypes.c_void_p
 A = P(1 << 20)  # an aligned address that is never read: these calls are refused on the host
+A2 = P(1 << 21)
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 
 
@@ -87,7 +88,7 @@ def test_rope_apply_refusals(lib):
 
 def append(lib, B=1, h_q=8, h_kv=2, s=1, d=64, d_rot=64, Lmax=32, dtype=0, q=A, kc=A, ws=A, ws_bytes=256, lens=A):
     st = strides(*([s * d] * 9))
-    return lib.gqa_rope_append(q, A, A, st, lens, None, A, A, kc, A, B, h_q, h_kv, s, d, d_rot, Lmax, 0, 1.0, dtype, ws,
+    return lib.gqa_rope_append(q, A, A, st, lens, None, A, A, kc, A2, B, h_q, h_kv, s, d, d_rot, Lmax, 0, 1.0, dtype, ws,
                                ws_bytes, None)
 
 
@@ -97,6 +98,7 @@ def test_append_refusals(lib):
     assert append(lib, Lmax=0) == INVALID
     assert append(lib, dtype=2) == UNSUPPORTED
     assert append(lib, kc=None) == INVALID
+    assert append(lib, kc=A2) == INVALID  # one cache for keys and values
     assert append(lib, lens=None) == INVALID
     assert append(lib, ws=None) == WORKSPACE
     assert append(lib, ws_bytes=255) == WORKSPACE
@@ -104,7 +106,7 @@ def test_append_refusals(lib):
     st = strides(*([64] * 9))
 
     def paged(page_size=16, max_pages=2, num_pages=4, table=A):
-        return lib.gqa_rope_append_paged(A, A, A, st, table, A, None, A, A, A, A, 1, 8, 2, 1, 64, 64, page_size,
+        return lib.gqa_rope_append_paged(A, A, A, st, table, A, None, A, A, A, A2, 1, 8, 2, 1, 64, 64, page_size,
                                          max_pages, num_pages, 0, 1.0, 0, None, 0, None)
     assert paged() == WORKSPACE  # everything else is in order
     assert paged(page_size=12) == INVALID
@@ -115,7 +117,7 @@ def test_append_refusals(lib):
     assert paged(page_size=1 << 20, max_pages=1 << 12) == INVALID
 
     def fp8(scale=A):
-        return lib.gqa_rope_append_fp8kv(A, A, A, st, scale, A, A, None, A, A, A, A, 1, 8, 2, 1, 64, 64, 32, 0, 1.0,
+        return lib.gqa_rope_append_fp8kv(A, A, A, st, scale, A, A, None, A, A, A, A2, 1, 8, 2, 1, 64, 64, 32, 0, 1.0,
                                          None, 0, None)
     assert fp8() == WORKSPACE
     assert fp8(scale=None) == INVALID
@@ -194,6 +196,9 @@ def test_evict_refusals(lib):
     assert evict(lib, ko=base, vo=base + (1 << 20), wo=base + (2 << 20)) == INVALID            # in place, Lout != Lmax
     assert evict(lib, ko=base, vo=base + (1 << 20), wo=base + (2 << 20), Lout=32) == WORKSPACE  # in place
     assert evict(lib, ko=base + 128) == INVALID             # overlaps k
+    assert evict(lib, ko=base + (4 << 20)) == INVALID       # k_out is v_out
+    assert evict(lib, ko=base + (4 << 20) - 128) == INVALID  # and a part of it
+    assert lib.gqa_evict_paged(A, A, A2, A, A, P(3 << 20), A, 1, 2, 64, 16, 2, 4, 8, 0, 0, 0, A, 256, None) == INVALID
     assert evict(lib, ko=base + (1 << 20) + 128) == INVALID  # overlaps v
     assert evict(lib, wo=base + (2 << 20) + 16) == INVALID  # overlaps the weights
     assert lib.gqa_evict_paged(A, A, A, A, A, P(1 << 21), A, 1, 2, 64, 16, 2, 4, 33, 0, 0, 0, A, 256, None) == INVALID
