@@ -16,7 +16,7 @@
 // Bound: HBM (about 0.75 operations per byte moved), or launch latency for a decode step.
 // A CTA takes a few consecutive tokens: their cos / sin tables are made once, in shared
 // memory, for all heads; then every thread keeps to one unit of a head -- VE pairs, two
-// 16-byte vectors -- and carries it through all tokens, four in flight, so that what depends
+// 16-byte vectors -- and carries it through all tokens, two in flight, so that what depends
 // on the head (which tensor, addresses, scale) is worked out once per head and what depends on
 // the token comes from shared memory.  While there are few tokens, the heads of one token are
 // spread over several CTAs instead.
@@ -58,11 +58,11 @@ struct RopeParams {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
-// Blocks per SM: as many as the registers of four units in flight allow without spilling.
+// Two units in flight per thread and as many blocks as the registers then allow: 2 x 4096 tokens of 32 + 8 heads of 128
+// take 38.3 us (39.2 with four units and six blocks, 40.4 with eight and four), their e4m3 chunk 21.5 (25.0, 30.1).
+constexpr int kRopeThreads = 128, kRopeBatch = 2;
 template <typename C>
-constexpr int rope_blocks() { return sizeof(C) == 1 ? 5 : 6; }
-constexpr int kRopeBatch = 4;  // units in flight per thread
+constexpr int rope_blocks() { return sizeof(C) == 1 ? 8 : 9; }  // per SM
 constexpr int kRopeMaxPairs = 256;
 constexpr int kRopeMaxTokens = 16, kRopeTable = 512;  // tokens per CTA, (cos, sin) pairs of its tables
 
