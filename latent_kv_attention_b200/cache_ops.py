@@ -75,6 +75,20 @@ def _strided(t, name, dtype, device):
     return st
 
 
+def _separate(out, os, x, xs, name, itself=False):
+    """out (strides os) shares no memory with x (strides xs), or, if `itself`, is x."""
+    a, b, e = out.data_ptr(), x.data_ptr(), x.element_size()
+    if itself and a == b and all(n == 1 or i == j for n, i, j in zip(x.shape, os, xs)):
+        _require(all(st != 0 or n == 1 for n, st in zip(x.shape, xs)), f"in place needs {name} without repeated rows")
+        return
+    if out.numel() and x.numel():
+        end_a, end_b = (at + e * (1 + sum((n - 1) * st for n, st in zip(t.shape, sts)))
+                        for t, at, sts in ((out, a, os), (x, b, xs)))
+        _require(a >= end_b or b >= end_a,
+                 f"the output must be {name} itself or share no memory with it" if itself else
+                 f"the output must share no memory with {name}")
+
+
 def _lens(cache_lens, B, device):
     return _dense(cache_lens, "cache_lens", torch.int32, device, (B,))
 
@@ -180,15 +194,11 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     pos = _dense(positions, "positions", torch.int32, dev, (B, s))
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    elif out is x or (out.data_ptr() == x.data_ptr() and out.stride() == xs):
-        _strided(out, "out", x.dtype, dev)
-        _require(out.shape == shape, "out must have x's shape")
-        _require(all(st != 0 or n == 1 for n, st in zip(shape, xs)), "in place needs x without repeated rows")
     else:
-        at, e = _dense(out, "out", x.dtype, dev, shape), x.element_size()
-        span = 1 + sum((n - 1) * st for n, st in zip(shape, xs)) if x.numel() else 0
-        _require(at >= x.data_ptr() + span * e or x.data_ptr() >= at + out.numel() * e,
-                 "out must be x itself or share no memory with it")
+        same = out is x or out.data_ptr() == x.data_ptr()
+        _strided(out, "out", x.dtype, dev) if same else _dense(out, "out", x.dtype, dev, shape)
+        _require(out.shape == shape, "out must have x's shape")
+        _separate(out, out.stride(), x, xs, "x", itself=True)
     os = out.stride()
     args = (x.data_ptr(), _I3(xs[0], xs[1], xs[2]), pos, freq, out.data_ptr(), _I3(os[0], os[1], os[2]), B, h, s, d,
             2 * inv_freq.numel(), bool(interleaved), bool(backward), amplitude, code)
@@ -200,6 +210,14 @@ def rope(x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1
     if rc:
         _check("rope_apply", rc)
     return out
+
+
+def _append_out(q_out, dt, dev, q, qs, k, ks, v, vs):
+    _dense(q_out, "q_out", dt, dev, q.shape)
+    os = q_out.stride()
+    _separate(q_out, os, q, qs, "the queries", itself=True)
+    _separate(q_out, os, k, ks, "the new keys")
+    _separate(q_out, os, v, vs, "the new values")
 
 
 def _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out):
@@ -215,7 +233,7 @@ def _append_operands(q, k, v, cache_lens, inv_freq, positions, q_out):
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _dense(q_out, "q_out", dt, dev, shape)
+        _append_out(q_out, dt, dev, q, qs, k, ks, v, vs)
     freq = _dense(inv_freq, "inv_freq", torch.float64, dev)
     return (dev, code, B, h_q, h_kv, s, d, q_out, _lens(cache_lens, B, dev), _positions(positions, B, s, dev), freq,
             2 * inv_freq.numel(), (q.data_ptr(), k.data_ptr(), v.data_ptr(), _I9(*qs[:3], *ks[:3], *vs[:3])))
@@ -238,7 +256,8 @@ def gqa_rope_append(q, k, v, k_cache, v_cache, cache_lens, inv_freq, positions=N
     """Rotary positions on a step's queries and keys, and its keys and values into the cache: q [B,h_q,s,d], k, v
     [B,h_kv,s,d] (strided views allowed); token t is written at row cache_lens[b] - s + t of k_cache, v_cache
     [B,h_kv,Lmax,d], and stands at that position unless positions int32 [B,s] says otherwise.  Tokens before row 0
-    are padding (not written, their query 0).  Returns the rotated queries [B,h_q,s,d] for gqa_attn."""
+    are padding (not written, their query 0).  Returns the rotated queries [B,h_q,s,d] for gqa_attn (q_out, contiguous,
+    where given: q itself, or memory of its own)."""
     dev, code, B, h_q, h_kv, s, d, q_out, lens, pos, freq, d_rot, qkv = _append_operands(
         q, k, v, cache_lens, inv_freq, positions, q_out)
     shape = _cache_shape(k_cache, B, h_kv, d)
@@ -291,7 +310,7 @@ def _latent_operands(q_r, c_kv, k_r, cache_lens, inv_freq, positions, q_out):
     if q_out is None:
         q_out = torch.empty_like(q_r, memory_format=torch.contiguous_format)
     else:
-        _dense(q_out, "q_out", dt, dev, shape)
+        _append_out(q_out, dt, dev, q_r, qs, c_kv, cs, k_r, ks)
     return (dev, code, B, h_q, s, c_kv.shape[3], d_r, q_out, _lens(cache_lens, B, dev),
             _positions(positions, B, s, dev), freq,
             (q_r.data_ptr(), c_kv.data_ptr(), k_r.data_ptr(), _I9(*qs[:3], *ks[:3], *cs[:3])))

@@ -120,6 +120,33 @@ def test_rope_refusals():
         lka.rope(buf[:-64].view(2, 3, 4, 64), pos, f, out=buf[64:].view(2, 3, 4, 64))
 
 
+def test_outputs_in_place_and_overlapping():
+    """out and q_out may be the rotated tensor itself, through any view of the same rows, and nothing else of it."""
+    g = gen(9)
+    B, h, s, d = 1, 4, 3, 64
+    f, _ = lka.rope_inv_freq(d)
+    pos = torch.arange(s, dtype=torch.int32, device=DEV).view(1, s)
+    buf = randn(g, (2 * h + 2) * s * d).bfloat16()
+    q, k, v = (buf[n * s * d:].as_strided((B, n2, s, d), (99 * 64, s * d, d, 1)) for n, n2 in ((0, h), (h, 2), (h + 2, 2)))
+    want = lka.rope(q, pos, f)
+    copy = buf.clone()
+    view = copy[:h * s * d].view(B, h, s, d)  # the same memory, another stride of the dimension of one
+    assert lka.rope(copy[:h * s * d].as_strided(q.shape, q.stride()), pos, f, out=view) is view
+    assert torch.equal(view, want)
+    assert torch.equal(copy[h * s * d:], buf[h * s * d:])
+    kc, vc = (torch.zeros((B, 2, 8, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    lens = torch.full((B,), s, dtype=torch.int32, device=DEV)
+    for q_out in (k.as_strided(q.shape, (h * s * d, s * d, d, 1)), v.as_strided(q.shape, (h * s * d, s * d, d, 1)),
+                  buf[d:].as_strided(q.shape, (h * s * d, s * d, d, 1))):
+        with pytest.raises(ValueError):
+            lka.gqa_rope_append(q, k, v, kc, vc, lens, f, q_out=q_out)
+    assert not kc.any() and torch.equal(want, lka.rope(q, pos, f))
+    want_k = lka.rope(k, pos, f)
+    q_out = buf[:h * s * d].view(B, h, s, d)
+    assert lka.gqa_rope_append(q, k, v, kc, vc, lens, f, q_out=q_out) is q_out
+    assert torch.equal(q_out, want) and torch.equal(kc[:, :, :s], want_k) and torch.equal(vc[:, :, :s], v)
+
+
 # ------------------------------------------------------------------ append
 def to_pool(x, page, g):
     """Cache [B,h,cap,d] -> pool with shuffled pages and its table."""
