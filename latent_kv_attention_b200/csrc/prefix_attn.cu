@@ -574,44 +574,53 @@ __global__ void __launch_bounds__(128) prefix_rows64_kernel(const PrefixParams p
 }
 
 // ---- fp32: CUDA cores ------------------------------------------------------------------------------------------
-// 16 query rows, four per warp; a tile of 32 keys, one key per lane for the scores, D / 32 value columns per lane.
-template <int D>
+// Bound by reads of shared memory (no fp32 tensor product exists): a warp takes RPW rows and 64 / KG of a tile's 64 keys,
+// so that a key vector feeds RPW multiply-adds and a query vector one per key lane.  16 rows: two warps of eight rows on
+// each quarter of the keys, two lanes a key; up to 4 rows: every warp all of them on an eighth.  The key groups of a row
+// keep sums of their own, joined once at the end.
+template <int D, int RPW, int KG>
 struct F32Cfg {
-    static constexpr int TK = 32, ROWS = 16, KROW = D + 4;  // padded key rows: 16-byte reads of 8 lanes hit all banks
-    static constexpr int SMEM = (ROWS * D + TK * KROW + TK * D + ROWS * TK) * 4;
+    static constexpr int TK = 64, KPW = TK / KG, LPK = 32 / KPW;  // keys per warp, lanes per key
+    static constexpr int WARPS = 8, THREADS = 32 * WARPS, BLOCKS = D == 64 ? 3 : 2;  // blocks per SM
+    static constexpr int ROWS = RPW * (WARPS / KG);
+    // 16 bytes behind each lane's part of a key or query, 16 behind the key: the reads of 8 lanes hit all banks
+    static constexpr int PART = D / LPK, KROW = D + 4 * LPK, QROW = D + 4 * LPK;
+    static constexpr int SMEM = (ROWS * QROW + TK * KROW + TK * D + WARPS * RPW * KPW) * 4;
+    static_assert(WARPS * RPW * (D + 2) <= TK * KROW, "the join fits the key tile");
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
-    using C = F32Cfg<D>;
+template <int D, int RPW, int KG>
+__global__ void __launch_bounds__(256, (F32Cfg<D, RPW, KG>::BLOCKS)) prefix_f32_kernel(const PrefixParams p) {
+    using C = F32Cfg<D, RPW, KG>;
     constexpr int VPL = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     float* qs = reinterpret_cast<float*>(smem);
-    float* ks = qs + C::ROWS * D;
+    float* ks = qs + C::ROWS * C::QROW;
     float* vs = ks + C::TK * C::KROW;
-    float* ps = vs + C::TK * D;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int row_w = warp / KG * RPW, key_w = warp % KG * C::KPW;  // the warp's first row and key
+    const int key = key_w + lane / C::LPK, sub = lane % C::LPK;     // the lane's key and its part of the head dim
+    float* ps = vs + C::TK * D + warp * RPW * C::KPW;
     Work w;
     pdl_trigger();
-    if (!find_work(p, C::ROWS, blockIdx.x, w, tid == 0)) return;
+    if (!find_work(p, C::ROWS, blockIdx.x, w, tid == 0)) {
+        pdl_wait();
+        return;
+    }
     const CacheRows rows = rows_of(p, w);
     const float* kb = static_cast<const float*>(w.prefix ? p.kp : p.k);
     const float* vb = static_cast<const float*>(w.prefix ? p.vp : p.v);
-    for (int i = tid; i < C::ROWS * (D / 4); i += 128) {
-        const int r = i / (D / 4), c = i % (D / 4);
+    for (int i = tid; i < C::ROWS * (D / 4); i += C::THREADS) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < w.nrows) x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + global_row(p, w, r) * D + c * 4);
-        *reinterpret_cast<float4*>(qs + r * D + c * 4) = x;
+        if (r < w.nrows) x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + global_row(p, w, r) * D + c);
+        *reinterpret_cast<float4*>(qs + r * C::QROW + c + c / C::PART * 4) = x;
     }
-    int vis[4];
+    int vis[RPW];
+    float m[RPW], l[RPW], o[RPW][VPL];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int rr = warp * 4 + r;
-        vis[r] = rr < w.nrows ? min(visible_end(p, w, rr), w.kend) : 0;
-    }
-    float m[4], l[4], o[4][VPL];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < RPW; ++r) {
+        vis[r] = row_w + r < w.nrows ? min(visible_end(p, w, row_w + r), w.kend) : 0;
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
@@ -619,74 +628,105 @@ __global__ void __launch_bounds__(128) prefix_f32_kernel(const PrefixParams p) {
     }
     for (int k0 = w.kbeg; k0 < w.kend; k0 += C::TK) {
         __syncthreads();
-        for (int i = tid; i < C::TK * (D / 4); i += 128) {
-            const int r = i / (D / 4), c = i % (D / 4);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (k0 + r < w.kend) {
-                const long long at = cache_row(rows, k0 + r, p.status) * D + c * 4;
-                x = *reinterpret_cast<const float4*>(kb + at);
-                y = *reinterpret_cast<const float4*>(vb + at);
-            }
-            *reinterpret_cast<float4*>(ks + r * C::KROW + c * 4) = x;
-            *reinterpret_cast<float4*>(vs + r * D + c * 4) = y;
+        for (int i = tid; i < C::TK * (D / 4); i += C::THREADS) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
+            const bool ok = k0 + r < w.kend;
+            const long long at = ok ? cache_row(rows, k0 + r, p.status) * D + c : 0;
+            cp_async16(smem_u32(ks + r * C::KROW + c + c / C::PART * 4), kb + at, ok);
+            cp_async16(smem_u32(vs + r * D + c), vb + at, ok);
         }
+        cp_async_commit();
+        cp_async_wait<0>();
         __syncthreads();
-        if (warp * 4 >= w.nrows) continue;  // a warp without rows only loads
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const float* kp = ks + lane * C::KROW;
-        const float* qp = qs + warp * 4 * D;
-#pragma unroll 8
-        for (int c = 0; c < D; c += 4) {
+        if (row_w >= w.nrows || k0 + key_w >= w.kend) continue;  // a warp without rows or keys only loads
+        float s[RPW] = {};
+        const float* kp = ks + key * C::KROW + sub * (C::PART + 4);
+        const float* qp = qs + row_w * C::QROW + sub * (C::PART + 4);
+#pragma unroll 4
+        for (int c = 0; c < C::PART; c += 4) {
             const float4 kv = *reinterpret_cast<const float4*>(kp + c);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 qv = *reinterpret_cast<const float4*>(qp + r * D + c);
+            for (int r = 0; r < RPW; ++r) {
+                const float4 qv = *reinterpret_cast<const float4*>(qp + r * C::QROW + c);
                 s[r] = fmaf(kv.x, qv.x, fmaf(kv.y, qv.y, fmaf(kv.z, qv.z, fmaf(kv.w, qv.w, s[r]))));
             }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float x = k0 + lane < vis[r] ? s[r] * p.scale_log2 : -INFINITY;
+        for (int r = 0; r < RPW; ++r) {
+#pragma unroll
+            for (int d = 1; d < C::LPK; d *= 2) s[r] += __shfl_xor_sync(0xffffffffu, s[r], d);
+            const float x = k0 + key < vis[r] ? s[r] * p.scale_log2 : -INFINITY;
             float mx = x;
 #pragma unroll
-            for (int d = 16; d; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            for (int d = 16; d >= C::LPK; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const float mn = fmaxf(m[r], mx);
             const float al = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
             const float e = mn == -INFINITY ? 0.f : exp2f(x - mn);
             m[r] = mn;
             l[r] = l[r] * al + e;
-            ps[(warp * 4 + r) * C::TK + lane] = e;
+            if (sub == 0) ps[r * C::KPW + lane / C::LPK] = e;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) o[r][i] *= al;
         }
         __syncwarp();
-#pragma unroll 4
-        for (int k = 0; k < C::TK; ++k) {
-            float v[VPL];
+        const float* vp = vs + key_w * D + lane * VPL;  // lane: value columns VPL * lane ..
+#pragma unroll 2
+        for (int k = 0; k < C::KPW; k += 4) {
+            float v[4][VPL];
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) v[i] = vs[k * D + i * 32 + lane];
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (VPL == 4)
+                    *reinterpret_cast<float4*>(v[e]) = *reinterpret_cast<const float4*>(vp + (k + e) * D);
+                else
+                    *reinterpret_cast<float2*>(v[e]) = *reinterpret_cast<const float2*>(vp + (k + e) * D);
+            }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float e = ps[(warp * 4 + r) * C::TK + k];
+            for (int r = 0; r < RPW; ++r) {
+                const float4 e = *reinterpret_cast<const float4*>(ps + r * C::KPW + k);
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) o[r][i] = fmaf(e, v[i], o[r][i]);
+                for (int i = 0; i < VPL; ++i)
+                    o[r][i] = fmaf(e.w, v[3][i], fmaf(e.z, v[2][i], fmaf(e.y, v[1][i], fmaf(e.x, v[0][i], o[r][i]))));
             }
         }
         __syncwarp();
     }
+    // every warp's rows side by side, then row by row the sum of its key groups
+    __syncthreads();
+    float* join = ks;  // [WARPS][RPW][D + 2]: values, maximum, sum
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int rr = warp * 4 + r;
+    for (int r = 0; r < RPW; ++r) {
         float sum = l[r];
 #pragma unroll
-        for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (rr >= w.nrows) continue;
-        const size_t at = global_row(p, w, rr) * p.n_slots + w.slot;
+        for (int d = 16; d >= C::LPK; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        float* at = join + (warp * RPW + r) * (D + 2);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) at[lane * VPL + i] = o[r][i];
+        if (lane == 0) {
+            at[D] = m[r];
+            at[D + 1] = sum;
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < min(C::ROWS, w.nrows); r += C::WARPS) {
+        const float* at = join + (r / RPW * KG * RPW + r % RPW) * (D + 2);  // key group g: RPW rows on
+        float mx = -INFINITY, sum = 0.f, acc[VPL] = {};
+#pragma unroll
+        for (int g = 0; g < KG; ++g) mx = fmaxf(mx, at[g * RPW * (D + 2) + D]);
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+            const float* part = at + g * RPW * (D + 2);
+            const float f = part[D] == -INFINITY ? 0.f : exp2f(part[D] - mx);
+            sum += f * part[D + 1];
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) acc[i] += f * part[lane * VPL + i];
+        }
+        const size_t to = global_row(p, w, r) * p.n_slots + w.slot;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) p.part_o[at * D + i * 32 + lane] = o[r][i] * inv;
-        if (lane == 0) p.part_lse[at] = sum > 0.f ? m[r] + log2f(sum) : -INFINITY;
+        for (int i = 0; i < VPL; ++i) p.part_o[to * D + lane * VPL + i] = acc[i] * inv;
+        if (lane == 0) p.part_lse[to] = sum > 0.f ? mx + log2f(sum) : -INFINITY;
     }
+    pdl_wait();  // the prefix's launch, before this one counts as done
 }
 
 // ---- the merge ---------------------------------------------------------------------------------------------------
@@ -844,6 +884,9 @@ int tc_keys(int pairs_heads, int Lp, double suffix_tiles, int d) {
     return cdiv(lt, best) * 128;
 }
 
+// Query rows of a block of prefix_f32_kernel where there are `rows`.
+int f32_rows(int rows) { return rows <= 4 ? 4 : rows <= 16 ? 16 : 32; }
+
 lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lmax, lka_dtype_t dtype, PrefixPlan* pl) {
     if (B < 0 || h_q < 1 || h_kv < 1 || s < 1 || d < 1 || Lp < 0 || Lmax < 1 || h_q % h_kv) return LKA_ERR_INVALID_ARG;
     if (dtype != LKA_BF16 && dtype != LKA_FP32) return LKA_ERR_UNSUPPORTED;
@@ -854,10 +897,18 @@ lka_status_t prefix_plan(int B, int h_q, int h_kv, int s, int d, int Lp, int Lma
     // Up to 16 query rows per KV head in all: prefix_stream_kernel, whose warps split the keys.  More, and the head dim
     // fits prefix_tc_kernel's tensor memory: that one.  d = 256: prefix_rows64_kernel, the prefix read once per 64 rows.
     pl->tc = !f32 && Bn * R > 16 && d <= 128;
-    pl->rows_pre = f32 || Bn * R <= 16 ? 16 : 64;
+    const int tile = 64;
+    const double slots = (double)sm_count() * (f32 ? (d == 128 ? 2 : 3) : d == 256 ? 1 : d == 128 ? 2 : 3);
+    pl->rows_pre = Bn * R <= 16 ? 16 : 64;
     pl->rows_suf = 16;
-    const int tile = f32 ? 32 : 64;
-    const double slots = (double)sm_count() * (f32 ? 3 : d == 256 ? 1 : d == 128 ? 2 : 3);
+    if (f32) {
+        // blocks of 32 rows for a prefix that keeps the SMs busy for a while (64 x 4 rows of 8 heads over 4096 keys: 247 us,
+        // 295 in 16s), of 16, and with suffixes of as many in one launch, for a short one (7 x 12 rows over 1001 keys:
+        // 15.3 us, 17.3 in 32s)
+        pl->rows_suf = f32_rows(R);
+        const bool own = (double)h_kv * cdiv(Bn * R, 16) * cdiv(Lp, tile) >= 4 * slots;
+        pl->rows_pre = own ? f32_rows(Bn * R) : std::max(pl->rows_suf, std::min(16, f32_rows(Bn * R)));
+    }
     const bool rows64 = !f32 && !pl->tc && Bn * R > 16;
     // the split knob, where it leaves at most kMaxSplits splits
     const int knob = split_tokens_knob();
@@ -952,10 +1003,38 @@ cudaError_t run_bf16(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
     return launch_merge<__nv_bfloat16, D>(p, st);
 }
 
+template <int D, int RPW, int KG>
+cudaError_t launch_f32(const PrefixParams& p, bool second, cudaStream_t st) {
+    using C = F32Cfg<D, RPW, KG>;
+    const cudaError_t e = allow_smem<prefix_f32_kernel<D, RPW, KG>>(C::SMEM);
+    const long long n = count_work(p, C::ROWS);
+    if (e != cudaSuccess || n == 0) return e;
+    if (n >= (1ll << 31)) return cudaErrorInvalidValue;
+    if (second) return launch_pdl<prefix_f32_kernel<D, RPW, KG>>(dim3((unsigned)n), C::THREADS, C::SMEM, st, p);
+    prefix_f32_kernel<D, RPW, KG><<<(unsigned)n, C::THREADS, C::SMEM, st>>>(p);
+    return cudaPeekAtLastError();
+}
+
 template <int D>
-cudaError_t run_f32(const PrefixParams& p, cudaStream_t st) {
+cudaError_t launch_f32_rows(const PrefixParams& p, int rows, bool second, cudaStream_t st) {
+    return rows == 4    ? launch_f32<D, 4, 8>(p, second, st)
+           : rows == 16 ? launch_f32<D, 8, 4>(p, second, st)
+                        : launch_f32<D, 8, 2>(p, second, st);
+}
+
+// Prefix and suffixes in one launch where their blocks have as many rows, else in two beside each other.
+template <int D>
+cudaError_t run_f32(PrefixParams p, const PrefixPlan& pl, cudaStream_t st) {
     TimedLaunch timer(st);
-    const cudaError_t e = launch_items<prefix_f32_kernel<D>>(F32Cfg<D>::SMEM, p, 16, st);
+    cudaError_t e = cudaSuccess;
+    const bool two = pl.rows_pre != pl.rows_suf && p.n_pre > 0;
+    if (two) {
+        p.do_suffix = 0;
+        e = launch_f32_rows<D>(p, pl.rows_pre, false, st);
+        p.do_prefix = 0;
+        p.do_suffix = 1;
+    }
+    if (e == cudaSuccess) e = launch_f32_rows<D>(p, pl.rows_suf, two, st);
     timer.stop();
     if (e != cudaSuccess) return e;
     return launch_merge<float, D>(p, st);
@@ -993,7 +1072,7 @@ lka_status_t prefix_run(PrefixParams& p, int d, float scale, lka_dtype_t dtype, 
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (dtype == LKA_FP32)
-        e = d == 64 ? run_f32<64>(p, st) : run_f32<128>(p, st);
+        e = d == 64 ? run_f32<64>(p, pl, st) : run_f32<128>(p, pl, st);
     else
         e = d == 64 ? run_bf16<64>(p, pl, st) : d == 128 ? run_bf16<128>(p, pl, st) : run_bf16<256>(p, pl, st);
     return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;

@@ -340,7 +340,10 @@ PREFIX = [  # B, h_q, h_kv, s, d, Lp, Lmax, causal, dtype, page
     (2, 8, 2, 5, 128, 64, 5, True, "bf16", 128), (33, 12, 4, 3, 128, 1500, 17, True, "bf16", 0),
     (2, 40, 2, 3, 128, 300, 50, True, "bf16", 0), (130, 8, 1, 1, 128, 2100, 9, False, "bf16", 16),
     (3, 8, 2, 1, 64, 200, 30, True, "fp32", 0), (2, 6, 3, 4, 128, 77, 20, True, "fp32", 8),
-    (9, 4, 1, 2, 64, 130, 40, False, "fp32", 16)]
+    (9, 4, 1, 2, 64, 130, 40, False, "fp32", 16), (1, 4, 1, 1, 128, 500, 60, True, "fp32", 0),
+    (40, 32, 8, 1, 128, 1300, 70, True, "fp32", 16), (3, 20, 2, 5, 64, 200, 90, True, "fp32", 0),
+    (2, 24, 2, 3, 128, 300, 100, False, "fp32", 8), (40, 16, 1, 2, 64, 5000, 33, True, "fp32", 0),
+    (3, 12, 1, 1, 64, 700, 200, True, "fp32", 0)]
 
 
 def prefix_case(case, seed, plen=None):
