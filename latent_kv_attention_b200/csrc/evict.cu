@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048, kKeep = 8;  // weights per thread that stay in registers
+constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -49,13 +50,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int cluster_load(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
 }
 __device__ __forceinline__ int2 cluster_load2(uint32_t addr, uint32_t rank) {
     uint32_t a;
@@ -84,9 +78,9 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool repor
 // One cluster of `cluster` blocks per (KV head, sequence); each block takes a contiguous part of the weights.  The
 // blocks add up one another's histograms through distributed shared memory and all come to the same threshold.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, const int cluster) {
-    __shared__ __align__(8) int hist[kBins];
+    __shared__ __align__(16) int hists[3][kBins];  // one per digit: none is cleared while another block may read it
     __shared__ int part[kSelWarps], part_eq[kSelWarps];
-    __shared__ int totals[2];  // this block's keys above the threshold, and equal to it
+    __shared__ __align__(8) int totals[2];  // this block's keys above the threshold, and equal to it
     __shared__ uint32_t s_prefix;
     __shared__ int s_need;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
@@ -129,9 +123,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     int need = chosen;  // of the keys whose higher digits equal prefix
     if (chosen > 0) {
         constexpr int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+        for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(hists)[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+#pragma unroll
         for (int d = 0; d < 3; ++d) {
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
+            int* hist = hists[d];
             const uint32_t mask = (1u << bits[d]) - 1;
             for_each([&](int, uint32_t u, bool in) {
                 if (in && (d == 0 || (u >> (shift[d] + bits[d])) == prefix)) atomicAdd(&hist[(u >> shift[d]) & mask], 1);
@@ -145,11 +141,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             int c0 = 0, c1 = 0;
             const int top = nb - 1 - 2 * tid;
             if (top >= 1) {
-                for (int r = 0; r < cluster; ++r) {
-                    const int2 two = cluster > 1 ? cluster_load2(smem_u32(&hist[top - 1]), r)
-                                                 : *reinterpret_cast<const int2*>(&hist[top - 1]);
-                    c0 += two.y;
-                    c1 += two.x;
+                if (cluster > 1) {
+                    int2 two[kMaxCluster];  // all on their way before the first is used
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r)
+                        two[r] = r < cluster ? cluster_load2(smem_u32(&hist[top - 1]), r) : make_int2(0, 0);
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r) {
+                        c0 += two[r].y;
+                        c1 += two[r].x;
+                    }
+                } else {
+                    const int2 two = *reinterpret_cast<const int2*>(&hist[top - 1]);
+                    c0 = two.y;
+                    c1 = two.x;
                 }
             }
             int sum = c0 + c1;
@@ -167,10 +172,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
                 s_prefix = (prefix << bits[d]) | (uint32_t)(second ? top - 1 : top);
                 s_need = need - before - (second ? c0 : 0);
             }
-            if (cluster > 1)
-                cluster_sync();  // nobody clears a histogram that another block still reads
-            else
-                __syncthreads();
+            __syncthreads();
             prefix = s_prefix;
             need = s_need;
         }
@@ -201,10 +203,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             }
         }
         cluster_sync();
-        for (int r = 0; r < rank; ++r) {
-            gt_before += cluster_load(smem_u32(&totals[0]), r);
-            eq_before += cluster_load(smem_u32(&totals[1]), r);
-        }
+        const int2 two = lane < rank ? cluster_load2(smem_u32(totals), lane) : make_int2(0, 0);
+        gt_before += __reduce_add_sync(0xffffffffu, two.x);
+        eq_before += __reduce_add_sync(0xffffffffu, two.y);
     }
     if (chosen > 0) {
         int at = sinks + gt_before + min(eq_before, need);
