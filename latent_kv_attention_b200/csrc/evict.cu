@@ -77,12 +77,12 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool repor
 
 // One cluster of `cluster` blocks per (KV head, sequence); each block takes a contiguous part of the weights.  The
 // blocks add up one another's histograms through distributed shared memory and all come to the same threshold.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, const int cluster) {
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams p, const int cluster) {
     __shared__ __align__(16) int hists[3][kBins];  // one per digit: none is cleared while another block may read it
     __shared__ int part[kSelWarps], part_eq[kSelWarps];
     __shared__ __align__(8) int totals[2];  // this block's keys above the threshold, and equal to it
     __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
+    __shared__ int s_need, s_whole;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int h = (int)blockIdx.x / cluster, b = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     pdl_trigger();
@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     if (chosen > 0) {
         constexpr int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
         for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(hists)[i] = make_int4(0, 0, 0, 0);
+        if (tid == 0) s_whole = 0;
         __syncthreads();
 #pragma unroll
         for (int d = 0; d < 3; ++d) {
@@ -171,10 +172,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
                 const bool second = before + c0 < need;
                 s_prefix = (prefix << bits[d]) | (uint32_t)(second ? top - 1 : top);
                 s_need = need - before - (second ? c0 : 0);
+                s_whole = s_need == (second ? c1 : c0) && s_prefix > 0;
             }
             __syncthreads();
             prefix = s_prefix;
             need = s_need;
+            if (s_whole) {  // the digit's keys all stay: no need to tell them apart (mostly so after two digits)
+                prefix = (prefix << shift[d]) - 1;
+                need = 0;
+                break;
+            }
         }
     }
     // Count, then write in order.  Keys above the threshold all stay, of those equal to it the first `need`.

@@ -640,6 +640,22 @@ def test_evict_nan_infinite_and_equal_weights():
     assert lka.gqa_evict(k, k, same, ints(10), 4, sinks=1, recent=1)[4][0, 0].tolist() == [0, 1, 2, 9]
 
 
+@pytest.mark.parametrize("L", [300, 20000, 70000])
+@pytest.mark.parametrize("kind", ["binades", "digits", "last"])
+def test_evict_thresholds_between_digits(L, kind):
+    """Weights that agree in their leading bits, cut at the border of a group of equal ones and one key beside it."""
+    i = torch.arange(L, device=DEV)
+    bits = {"binades": lambda: (120 + i % 8) << 23, "digits": lambda: (0x3f800000 + (i % 16 << 10)),
+            "last": lambda: 0x3f800000 + i * 7 % 5}[kind]().to(torch.int32)
+    w = bits.view(torch.float32).view(1, 1, L).contiguous()
+    k = torch.zeros((1, 1, L, 16), dtype=torch.bfloat16, device=DEV)
+    order = torch.argsort(w[0, 0], descending=True, stable=True)
+    group = int((w == w.max()).sum())
+    for budget in (1, group - 1, group, group + 1, 3 * group, 3 * group + 1, L - 1):
+        kept = lka.gqa_evict(k, k, w, ints(L), budget)[4]
+        assert torch.equal(kept[0, 0].long(), order[:budget].sort().values), budget
+
+
 def test_evict_empty_and_bad_lengths():
     g, k, v, w, _ = evict_case((3, 2, 64, 50, 20, 1, 1, "bf16"), 4)
     ko, vo, wo, new, kept = lka.gqa_evict(k, v, w, ints(0, 1, 50), 20)
