@@ -370,9 +370,9 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     p.status = static_cast<uint32_t*>(ws);
     const cudaStream_t st = (cudaStream_t)stream;
     // Up to 8192 weights a row fits one block's registers.  A longer row is shared by a cluster while all clusters run
-    // at once (whole call, 32 rows of 17,600 weights: 25 us alone, 18 in fours; 8 of 65,536: 85, 34 in fours, 23 in
-    // eights), but clusters of eight blocks of 1024 threads find few places (32 rows: 53 us), nor do fours past the
-    // number of SMs (56 rows of 17,600: 25 us alone, 31 in fours).
+    // at once (both kernels: 32 rows of 17,600 weights 25 us alone, 20 in fours; 8 of 65,536: 82, 33 in fours, 21 in
+    // eights), but clusters of eight blocks of 1024 threads find few places (32 rows: 45 us), nor do fours past the
+    // number of SMs (56 rows of 17,600: 29 us alone, 34 in fours).
     const long long rows = (long long)p.B * p.h_kv;
     int cluster = 1;
     if (p.Lmax > 4 * kKeep * kSelThreads && rows <= 8)
