@@ -176,7 +176,9 @@ __global__ void __launch_bounds__(kwt::NT, kwt::Cfg<D>::CTAS)
                 for (int k = 0; k < D / 16; ++k)
                     umma_ss(tmem + buf * 128, kd + (k / 4) * B4 + (k % 4) * 2, qd + (k / 4) * B4 + (k % 4) * 2, idesc, k != 0);
                 umma_commit(smem_u32(&s_ready[buf]));
-                umma_commit(smem_u32(&empty[s]));
+                // only where the loader waits for it: an arrival that nobody waits for may find the CTA's shared memory
+                // in other hands
+                if (i + C::NS < n_mine) umma_commit(smem_u32(&empty[s]));
             }
             if (!ok) s_abort = 1;
         }

@@ -182,6 +182,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
         }
     } else if (warp >= W_MMA && warp < W_MMA + 2 * n_qt) {
         // ------------------------------ MMA issuers ------------------------------
+        // Every commit's arrival is waited for before the CTA ends (one that nobody waits for may find its shared memory
+        // in other hands): stages are released only where the loader fills them again, the last product is o_done's.
         const int i = (warp - W_MMA) / 2;
         constexpr int B4 = C::BOX >> 4, T4 = C::TILE >> 4, H4 = TB * 128 >> 4;
         const uint32_t ts = tmem + C::T_S + 2 * i * TB, to = tmem + C::T_O + i * D;
@@ -203,7 +205,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                             k != 0);
                 umma_commit(smem_u32(&s_ready[2 * i + (n & 1)]));
                 if ((n & 1) || n == nb - 1) {
-                    umma_commit(smem_u32(&empty[st]));
+                    // (K tile n / 2 is copy 2 (n / 2) of the ring)
+                    if ((n & ~1) + C::NS < 2 * n_kt) umma_commit(smem_u32(&empty[st]));
                     st += 2;
                     if (st >= C::NS) {
                         st -= C::NS;
@@ -211,6 +214,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
                     }
                 }
             }
+            // the last product but one, for which no later block waits
+            if (ok && nb > 1) ok = mbar_wait(smem_u32(&o_ready[2 * i + (nb & 1)]), ((nb - 2) >> 1) & 1, p.status);
             if (!ok) s_abort = 1;
         } else if (lane == 0) {  // O_i += P_i(n) V_n
             constexpr uint32_t idesc = idesc_bf16_f32(128, D, false, true);
@@ -228,10 +233,9 @@ __global__ void __launch_bounds__(ptc::NT, 1)
 #pragma unroll
                 for (int k = 0; k < TB / 16; ++k)
                     umma_ts(to, ts + (n & 1) * TB + k * 8, vd + k * (2048 >> 4), idesc, (n | k) != 0);
-                umma_commit(smem_u32(&o_ready[2 * i + (n & 1)]));
-                if (n == nb - 1) umma_commit(smem_u32(&o_done[i]));
+                umma_commit(smem_u32(n == nb - 1 ? &o_done[i] : &o_ready[2 * i + (n & 1)]));
                 if ((n & 1) || n == nb - 1) {
-                    umma_commit(smem_u32(&empty[st]));
+                    if ((n & ~1) + 1 + C::NS < 2 * n_kt) umma_commit(smem_u32(&empty[st]));
                     st += 2;
                     if (st >= C::NS) {
                         st -= C::NS;
