@@ -469,12 +469,12 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
 #pragma unroll
             for (int k = 0; k < 4; ++k) M = fmaxf(M, ml[k * 16 + r]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum += M == -INFINITY ? 0.f : fast_exp2(ml[k * 16 + r] - M) * ml[64 + k * 16 + r];
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            for (int k = 0; k < 4; ++k) sum += fast_exp2(ml[k * 16 + r] - (M == -INFINITY ? 0.f : M)) * ml[64 + k * 16 + r];
+            const float inv = part_inverse(sum);
             const float4 x = *reinterpret_cast<const float4*>(om + r * C::OROW + c * 4);
             const size_t to = global_row(p, w, r) * p.n_slots + w.slot;
             *reinterpret_cast<float4*>(p.part_o + to * D + c * 4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-            if (c == 0) p.part_lse[to] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+            if (c == 0) p.part_lse[to] = part_normaliser(M, sum);
         }
         named_barrier(1, 128);  // the buffers are free for the next item
         if (!ok) s_abort = 1;
@@ -564,12 +564,12 @@ __global__ void __launch_bounds__(128) prefix_rows64_kernel(const PrefixParams p
         const int r = row_w + g + 8 * h;
         if (r >= w.nrows) continue;
         const size_t at = global_row(p, w, r) * p.n_slots + w.slot;
-        const float inv = st.l[h] > 0.f ? 1.f / st.l[h] : 0.f;
+        const float inv = part_inverse(st.l[h]);
         float* po = p.part_o + at * D;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
             *reinterpret_cast<float2*>(po + i * 8 + 2 * t) = make_float2(st.o[i][2 * h] * inv, st.o[i][2 * h + 1] * inv);
-        if (t == 0) p.part_lse[at] = st.l[h] > 0.f ? st.m[h] + log2f(st.l[h]) : -INFINITY;
+        if (t == 0) p.part_lse[at] = part_normaliser(st.m[h], st.l[h]);
     }
 }
 
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(256, (F32Cfg<D, RPW, KG>::BLOCKS)) prefix_f32_
             for (int d = 16; d >= C::LPK; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const float mn = fmaxf(m[r], mx);
             const float al = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
-            const float e = mn == -INFINITY ? 0.f : exp2f(x - mn);
+            const float e = x == -INFINITY ? 0.f : exp2f(mn == -INFINITY ? x : x - mn);  // (a NaN score moves no maximum)
             m[r] = mn;
             l[r] = l[r] * al + e;
             if (sub == 0) ps[r * C::KPW + lane / C::LPK] = e;
@@ -723,10 +723,10 @@ __global__ void __launch_bounds__(256, (F32Cfg<D, RPW, KG>::BLOCKS)) prefix_f32_
             for (int i = 0; i < VPL; ++i) acc[i] += f * part[lane * VPL + i];
         }
         const size_t to = global_row(p, w, r) * p.n_slots + w.slot;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = part_inverse(sum);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) p.part_o[to * D + lane * VPL + i] = acc[i] * inv;
-        if (lane == 0) p.part_lse[to] = sum > 0.f ? mx + log2f(sum) : -INFINITY;
+        if (lane == 0) p.part_lse[to] = part_normaliser(mx, sum);
     }
     pdl_wait();  // the prefix's launch, before this one counts as done
 }
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < kMaxSlots / 32; ++k) {
-        const float f = M == -INFINITY ? 0.f : exp2f(x[k] - M);
+        const float f = x[k] == -INFINITY ? 0.f : exp2f(x[k] - M);
         fs[warp][k * 32 + lane] = f;
         sum += f;
     }
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 #pragma unroll
             for (int e = 0; e < VPL; ++e) a[e] += others[k][lane * VPL + e];
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = part_inverse(sum);
     T* out = static_cast<T*>(p.out) + row * D + lane * VPL;
     if constexpr (sizeof(T) == 2) {
         uint32_t u[VPL / 2];
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
 #pragma unroll
         for (int e = 0; e < VPL; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
     }
-    if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = part_normaliser(M, sum) * 0.69314718055994530942f;
 }
 
 template <typename T, int D>

@@ -1,6 +1,8 @@
 // prefix_attn.h -- parameters of the shared-prefix attention kernels.
 #pragma once
 
+#include <math.h>
+
 #include "../../include/lka.h"
 #include "common.cuh"
 
@@ -43,5 +45,10 @@ __device__ __forceinline__ int prefix_length(const PrefixParams& p, bool report)
     }
     return P;
 }
+
+// A part of a row, from its maximum and the sum of its exponentials: the sum is 0 where no key counts, and NaN (which the
+// row's output and normaliser then are, as in gqa_attn) where a score is NaN.
+__device__ __forceinline__ float part_inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float part_normaliser(float m, float sum) { return sum == 0.f ? -INFINITY : m + log2f(sum); }
 
 }  // namespace lka

@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(ptc::NT, 1)
         const int b = g.per_seq > 1 ? t / g.per_seq : t * g.seqs + r / p.R, gr = g.per_seq > 1 ? t % g.per_seq * g.rows + r : r % p.R;
         const bool mine = ok && r < g.rows && b < p.B && gr < p.R;
         const long long at = mine ? (long long)((((size_t)b * p.h_kv + kvh) * p.R + gr) * p.n_slots + split) : -1;
-        const float l = l2.x + l2.y, inv = l > 0.f ? 1.f / l : 0.f;
-        if (mine) p.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+        const float l = l2.x + l2.y, inv = part_inverse(l);
+        if (mine) p.part_lse[at] = part_normaliser(m, l);
         // O leaves through this warp's quarter of the row tile's query buffer (its products are done), half of the
         // columns at a time: rows written by their lanes in 16-byte chunks, permuted over the banks, and read back row
         // by row (a lane writing its own row of the result touches 32 rows per instruction: 12,000 cycles per CTA)
