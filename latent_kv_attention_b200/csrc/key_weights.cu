@@ -140,7 +140,10 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
                 const float2 l2 = *reinterpret_cast<const float2*>(lb + r0 + 2 * t);
                 float e[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = fast_exp2(fmaf(acc[i], p.scale_log2, i & 1 ? -l2.y : -l2.x));
+                for (int i = 0; i < 4; ++i) {
+                    const float l = i & 1 ? l2.y : l2.x;
+                    e[i] = l == INFINITY ? 0.f : fast_exp2(fmaf(acc[i], p.scale_log2, -l));  // (an empty row may score NaN)
+                }
                 if (masked || r0 + 8 > n) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(128) key_weights_f32_kernel(const KeyWeightPar
             for (int r = 0; r < RB / 2; ++r) {
                 const int rr = half * (RB / 2) + r;
                 const int last = p.causal ? L - p.s + (first + rr) % p.s : L - 1;
-                if (rr < n && key <= last && key < L) w += exp2f(fmaf(acc[r], p.scale_log2, -ls[rr]));
+                if (rr < n && key <= last && key < L && ls[rr] != INFINITY) w += exp2f(fmaf(acc[r], p.scale_log2, -ls[rr]));
             }
         }
     if (half) red[kk] = w;

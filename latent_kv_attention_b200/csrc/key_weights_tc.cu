@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(kwt::NT, kwt::Cfg<D>::CTAS)
         fetch(grp);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-        // one score tile, 16 columns at a time; MASK: rows before `first` do not see the key
+        // one score tile, 16 columns at a time; MASK: rows before `first` do not see the key, and rows without keys, whose
+        // queries may be NaN, give nothing (elsewhere finite scores less the infinite normaliser do that)
         auto tile = [&](auto mask, uint32_t ts, const float* lb, int first, uint32_t release) {
             constexpr bool MASK = decltype(mask)::value;
             uint32_t sr[2][16];
@@ -230,10 +231,10 @@ __global__ void __launch_bounds__(kwt::NT, kwt::Cfg<D>::CTAS)
                     float2 e0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
                     float2 e1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
                     if constexpr (MASK) {
-                        if (16 * q + c < first) e0.x = 0.f;
-                        if (16 * q + c + 1 < first) e0.y = 0.f;
-                        if (16 * q + c + 2 < first) e1.x = 0.f;
-                        if (16 * q + c + 3 < first) e1.y = 0.f;
+                        if (16 * q + c < first || l4.x == -INFINITY) e0.x = 0.f;
+                        if (16 * q + c + 1 < first || l4.y == -INFINITY) e0.y = 0.f;
+                        if (16 * q + c + 2 < first || l4.z == -INFINITY) e1.x = 0.f;
+                        if (16 * q + c + 3 < first || l4.w == -INFINITY) e1.y = 0.f;
                     }
                     acc[0] = __fadd2_rn(acc[0], e0);
                     acc[1] = __fadd2_rn(acc[1], e1);
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(kwt::NT, kwt::Cfg<D>::CTAS)
             float* lb = ls + (turn & 1) * TQ;
 #pragma unroll
             for (int k = 0; k < TQ / 32; ++k) lb[32 * k + lane] = next[k] == -INFINITY ? -INFINITY : -next[k] * kLog2e;
-            __syncwarp();
+            const bool empty = __any_sync(0xffffffffu, fminf(fminf(next[0], next[1]), fminf(next[2], next[3])) == -INFINITY);
+            static_assert(TQ / 32 == 4, "the rows above");
             fetch(i + NG);
             const int buf = i % NBUF;
             if (ok) ok = mbar_wait(smem_u32(&s_ready[buf]), (i / NBUF) & 1, p.status);
@@ -253,8 +255,8 @@ __global__ void __launch_bounds__(kwt::NT, kwt::Cfg<D>::CTAS)
             const int n = (int)rank + i * cluster, t0 = start + n % per * TQ;
             const uint32_t ts = tmem + lanes + buf * 128, release = smem_u32(&s_free[buf]);
             // query t sees key j when j <= L - s + t: a tile whose first query sees the last key needs no mask
-            if (p.causal && j0 + TK - 1 > L - p.s + t0)
-                tile(std::true_type{}, ts, lb, key - (L - p.s) - t0, release);
+            if (empty || (p.causal && j0 + TK - 1 > L - p.s + t0))
+                tile(std::true_type{}, ts, lb, p.causal ? key - (L - p.s) - t0 : 0, release);
             else
                 tile(std::false_type{}, ts, lb, 0, release);
         }

@@ -34,3 +34,23 @@ def test_nan_reaches_the_rows_it_reaches_in_gqa_attn(B, d, dtype, where):
     assert ref_lse.isnan().any()
     assert torch.equal(lse.isnan(), ref_lse.isnan()) and torch.equal(out.isnan(), ref.isnan())
     assert not lse.isinf().any()
+
+
+@pytest.mark.parametrize("s,dtype,d,causal", [(1, "bf16", 128, True), (3, "bf16", 256, True), (40, "bf16", 64, False),
+                                              (130, "bf16", 64, True), (300, "bf16", 128, False), (70, "bf16", 256, True),
+                                              (3, "fp32", 64, True), (40, "fp32", 128, False)])
+def test_weights_of_empty_rows_that_hold_nan(s, dtype, d, causal):
+    """Rows whose lse is -inf add nothing to any key, even where their queries are NaN or infinite."""
+    g = gen(4)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v = (randn(g, 2, h, n, d, dtype=dt) for h, n in ((8, s), (2, 350), (2, 350)))
+    lens = ints(350, 310)
+    _, lse = lka.gqa_attn(q, k, v, lens, causal=causal, return_lse=True)
+    for row in ((0, 1, 0), (1, 7, s - 1), (1, 2, s // 2)):
+        lse[row] = -math.inf
+    want = lka.gqa_key_weights(q, k, lse, lens, causal=causal)
+    assert not want.isnan().any()
+    for bad in (math.nan, math.inf, -math.inf):
+        for row in ((0, 1, 0), (1, 7, s - 1), (1, 2, s // 2)):
+            q[row] = bad
+        assert torch.equal(lka.gqa_key_weights(q, k, lse, lens, causal=causal), want)
