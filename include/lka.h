@@ -472,6 +472,9 @@ LKA_API lka_status_t gqa_evict_paged(void *k_pages, void *v_pages, float *weight
 LKA_API lka_status_t lka_device_status(const void *ws, void *stream);
 /* Enqueues a reset of the workspace status word to LKA_OK on `stream`. */
 LKA_API lka_status_t lka_clear_status(void *ws, void *stream);
+/* Enqueues on `stream`: the flags raised in workspace ws are raised in the status word of `to` as well, atomically (for
+ * a scratch workspace whose contents do not outlive the call, as in a captured graph). */
+LKA_API lka_status_t lka_add_status(void *to, const void *ws, void *stream);
 /* Human-readable name of a status code (static string, never NULL). */
 LKA_API const char *lka_status_string(lka_status_t status);
 /* Split size (KV tokens per CTA) for the split-KV kernels of the calls made FROM THE CALLING HOST THREAD;

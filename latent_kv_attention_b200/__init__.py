@@ -97,6 +97,7 @@ SIGNATURES = {
     "gqa_evict_paged": (_I, [_P] * 7 + [_I] * 10 + [_P, _Z, _P]),
     "lka_device_status": (_I, [_P, _P]),
     "lka_clear_status": (_I, [_P, _P]),
+    "lka_add_status": (_I, [_P, _P, _P]),
     "lka_status_string": (ctypes.c_char_p, [_I]),
     "lka_set_split_tokens": (_I, [_I]),
     "lka_selftest_wait_timeout": (_I, [_P, _Z, _I, _P]),

@@ -144,7 +144,7 @@ def _call(name, device, args, sizes=None):
         ws[:_HEADER].zero_()
         rc = f(*args, ws.data_ptr(), ws.numel(), stream)
         # the captured call's flags outlive its scratch
-        captured_status(device, create=True)[:4].view(torch.int32).bitwise_or_(ws[:4].view(torch.int32))
+        rc = rc or _function("lka_add_status")(captured_status(device, create=True).data_ptr(), ws.data_ptr(), stream)
     if rc:
         _check(name, rc)
 

@@ -1,0 +1,52 @@
+"""Status words, workspaces and captured graphs of the cache operators (marked gpu): what one call raises or leaves
+behind, no other call loses, clears or takes for its own."""
+import pytest
+import torch
+
+import latent_kv_attention_b200 as lka
+from test_gpu_cache_ops import DEV, gen, prefix_case, randn
+
+pytestmark = pytest.mark.gpu
+BAD_LENGTH = 6
+
+
+@pytest.fixture(autouse=True)
+def _clear_status():
+    lka.clear_status()
+    yield
+    lka.clear_status()
+
+
+def append_args(length, B=2):
+    """Operands of a gqa_rope_append of one token per sequence into caches of 16 rows."""
+    g = gen(1)
+    f, _ = lka.rope_inv_freq(64)
+    q, k = randn(g, B, 4, 1, 64), randn(g, B, 2, 1, 64)
+    kc, vc = randn(g, B, 2, 16, 64), randn(g, B, 2, 16, 64)
+    return q, k, k, kc, vc, torch.full((B,), length, dtype=torch.int32, device=DEV), f
+
+
+def captured(call):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    return g
+
+
+def test_graphs_that_replay_together_lose_no_flag():
+    """One graph raises a flag in the shared header while another adds the (empty) flags of its calls to it."""
+    q, kp, vp, k, v, lens, _, _ = prefix_case((2, 4, 2, 1, 64, 64, 30, True, "bf16", 0), 1)
+    a = append_args(17)
+    lka.gqa_rope_append(*a)
+    lka.gqa_attn_shared_prefix(q, kp, vp, k, v, lens)
+    raises = captured(lambda: lka.gqa_rope_append(*a))
+    adds = captured(lambda: [lka.gqa_attn_shared_prefix(q, kp, vp, k, v, lens) for _ in range(30)])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(500):
+        lka.clear_status()
+        torch.cuda.synchronize()
+        for s, g in zip(streams, (adds, raises)):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert lka.device_status() == BAD_LENGTH
