@@ -472,6 +472,11 @@ LKA_API lka_status_t gqa_evict_paged(void *k_pages, void *v_pages, float *weight
 LKA_API lka_status_t lka_device_status(const void *ws, void *stream);
 /* Enqueues a reset of the workspace status word to LKA_OK on `stream`. */
 LKA_API lka_status_t lka_clear_status(void *ws, void *stream);
+/* The status header of the current device for calls captured into CUDA graphs, whose own workspace may end with the
+ * graph: 256 bytes inside the library, zero at the start, at one address until the process exits.  Any number of
+ * captured calls may raise their flags in it; lka_device_status and lka_clear_status take it as a workspace.  May be
+ * called while a stream captures.  NULL without a device. */
+LKA_API void *lka_captured_header(void);
 /* Enqueues on `stream`: the flags raised in workspace ws are raised in the status word of `to` as well, atomically (for
  * a scratch workspace whose contents do not outlive the call, as in a captured graph). */
 LKA_API lka_status_t lka_add_status(void *to, const void *ws, void *stream);

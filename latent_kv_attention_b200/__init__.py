@@ -95,6 +95,7 @@ SIGNATURES = {
     "gqa_key_weights_paged": (_I, [_P] * 6 + [_I] * 10 + [_F, _I, _P, _Z, _P]),
     "gqa_evict": (_I, [_P] * 9 + [_I] * 9 + [_P, _Z, _P]),
     "gqa_evict_paged": (_I, [_P] * 7 + [_I] * 10 + [_P, _Z, _P]),
+    "lka_captured_header": (_P, []),
     "lka_device_status": (_I, [_P, _P]),
     "lka_clear_status": (_I, [_P, _P]),
     "lka_add_status": (_I, [_P, _P, _P]),
@@ -551,7 +552,7 @@ def device_status(device=None) -> int:
     code = int(library().lka_device_status(_ptr(ws), _stream_ptr()))
     captured = cache_ops.captured_status(device)
     if code == LKA_OK and captured is not None:
-        code = int(library().lka_device_status(_ptr(captured), _stream_ptr()))
+        code = int(library().lka_device_status(captured, _stream_ptr()))
     return code
 
 
@@ -561,7 +562,7 @@ def clear_status(device=None):
     _check("lka_clear_status", library().lka_clear_status(_ptr(ws), _stream_ptr()))
     captured = cache_ops.captured_status(device)
     if captured is not None:
-        _check("lka_clear_status", library().lka_clear_status(_ptr(captured), _stream_ptr()))
+        _check("lka_clear_status", library().lka_clear_status(captured, _stream_ptr()))
 
 
 def gqa_split_count(B: int, h_q: int, h_kv: int, s_q: int, d: int, Lmax: int, dtype=torch.bfloat16) -> int:

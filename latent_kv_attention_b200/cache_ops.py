@@ -30,14 +30,18 @@ _captured_lock = threading.Lock()
 
 
 def captured_status(device, create=False):
-    """The status header that captured calls on `device` raise their flags in (None before the first one): one per
-    device, never replaced, because a graph keeps its address."""
+    """The address of the status header that captured calls on `device` raise their flags in (None before the first one):
+    one per device, of the library's, because a graph keeps the address and no graph may own or clear the header."""
     index = device.index if device.index is not None else torch.cuda.current_device()
     with _captured_lock:
-        t = _captured.get(index)
-        if t is None and create:
-            t = _captured[index] = torch.zeros(_HEADER, dtype=torch.uint8, device=device)
-        return t
+        address = _captured.get(index)
+        if address is None and create:
+            with torch.cuda.device(index):
+                address = library().lka_captured_header()
+            if not address:
+                raise RuntimeError(f"no status header on cuda:{index}")
+            _captured[index] = address
+        return address
 
 
 # The checks below run on every call, a decode step's included: they compare first and word the message only when
@@ -127,8 +131,6 @@ def _call(name, device, args, sizes=None):
             return _call(name, device, args, sizes)
     f, stream = _function(name), _stream_now(index)
     if not _capturing():
-        if index not in _captured:
-            captured_status(device, create=True)  # outside a graph, so that no replay clears it
         ws = workspaces._ws.get((index, stream))
         if ws is None:
             ws = workspaces.get(_HEADER, device)
@@ -137,14 +139,13 @@ def _call(name, device, args, sizes=None):
             ws = workspaces.get(_function(name + "_workspace_size")(*sizes), device)
             rc = f(*args, ws.data_ptr(), ws.numel(), stream)
     elif sizes is None:
-        ws = captured_status(device, create=True)
-        rc = f(*args, ws.data_ptr(), ws.numel(), stream)
+        rc = f(*args, captured_status(device, create=True), _HEADER, stream)
     else:
         ws = torch.empty(max(_function(name + "_workspace_size")(*sizes), _HEADER), dtype=torch.uint8, device=device)
         ws[:_HEADER].zero_()
         rc = f(*args, ws.data_ptr(), ws.numel(), stream)
         # the captured call's flags outlive its scratch
-        rc = rc or _function("lka_add_status")(captured_status(device, create=True).data_ptr(), ws.data_ptr(), stream)
+        rc = rc or _function("lka_add_status")(captured_status(device, create=True), ws.data_ptr(), stream)
     if rc:
         _check(name, rc)
 

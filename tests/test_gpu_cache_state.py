@@ -1,5 +1,9 @@
 """Status words, workspaces and captured graphs of the cache operators (marked gpu): what one call raises or leaves
 behind, no other call loses, clears or takes for its own."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -8,6 +12,7 @@ from test_gpu_cache_ops import DEV, gen, prefix_case, randn
 
 pytestmark = pytest.mark.gpu
 BAD_LENGTH = 6
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(autouse=True)
@@ -50,3 +55,50 @@ def test_graphs_that_replay_together_lose_no_flag():
                 g.replay()
         torch.cuda.synchronize()
         assert lka.device_status() == BAD_LENGTH
+
+
+CAPTURE_FIRST = """
+import sys
+sys.path[:0] = ["tests", "."]
+import torch
+import latent_kv_attention_b200 as lka
+from test_gpu_cache_ops import gen, ints, randn
+g = gen(1)
+sets = []
+f = torch.ones(32, dtype=torch.float64, device="cuda")
+for i in range(2):
+    q, k = randn(g, 1, 4, 1, 64), randn(g, 1, 2, 1, 64)
+    sets.append((q, k, k.clone(), randn(g, 1, 2, 16, 64), randn(g, 1, 2, 16, 64), ints(3), f))
+p = randn(g, 2, 100, 64)
+junk = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+del junk
+torch.cuda.synchronize()
+torch.cuda.empty_cache()  # what the graphs allocate may hold anything
+graphs = []
+for s in sets:
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        q = lka.gqa_rope_append(*s)
+        lka.gqa_attn_shared_prefix(q, p, p, s[3], s[4], s[5])
+    graphs.append(gr)
+seen = [lka.device_status()]
+for gr in graphs:
+    gr.replay()
+seen.append(lka.device_status())
+sets[1][5].fill_(99)
+graphs[1].replay()
+graphs[0].replay()
+seen.append(lka.device_status())
+lka.clear_status()
+graphs[0].replay()
+seen.append(lka.device_status())
+print(*seen)
+"""
+
+
+def test_first_calls_of_a_process_in_captures():
+    """Graphs captured before any eager call: no status before the first replay, and a replay of one clears no flag of
+    another's."""
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    assert r.stdout.split() == ["0", "0", str(BAD_LENGTH), "0"]
