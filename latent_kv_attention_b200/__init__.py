@@ -149,8 +149,9 @@ def _ptr(t):
 class _Workspaces:
     """One zero-initialised device workspace per (device, stream), grown on demand.
 
-    The first 256 bytes of a workspace hold the library's sticky status word;
-    the rest is scratch that the kernels overwrite on every call."""
+    The first 256 bytes of a workspace hold the library's sticky status word,
+    which a larger workspace takes over from the one it replaces; the rest is
+    scratch that the kernels overwrite on every call."""
 
     def __init__(self):
         self._ws = {}
@@ -163,7 +164,10 @@ class _Workspaces:
         with self._lock:
             t = self._ws.get(key)
             if t is None or t.numel() < nbytes:
-                t = torch.zeros(nbytes + (1 << 20), dtype=torch.uint8, device=device)
+                old, t = t, torch.zeros(nbytes + (1 << 20), dtype=torch.uint8, device=device)
+                # (a copy that a capture recorded would bring the old flags back with every replay)
+                if old is not None and not (t.is_cuda and torch.cuda.is_current_stream_capturing()):
+                    t[:4].copy_(old[:4])
                 self._ws[key] = t
             return t
 

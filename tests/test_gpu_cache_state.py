@@ -102,3 +102,21 @@ def test_first_calls_of_a_process_in_captures():
     r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-3000:]
     assert r.stdout.split() == ["0", "0", str(BAD_LENGTH), "0"]
+
+
+@pytest.mark.parametrize("later", ["prefix", "gqa_attn"])
+def test_status_outlives_the_growth_of_a_workspace(later):
+    """The flags of a call on a small workspace are still there when a later call on the stream needs a larger one."""
+    with torch.cuda.stream(torch.cuda.Stream()):
+        lka.gqa_rope_append(*append_args(17))
+        q, kp, vp, k, v, lens, _, _ = prefix_case((64, 32, 8, 1, 128, 4000, 30, True, "bf16", 0), 1)
+        before = lka.workspaces.get(256, q.device)
+        if later == "prefix":
+            lka.gqa_attn_shared_prefix(q, kp, vp, k, v, lens)
+        else:
+            kk = torch.randn(2, 8, 60000, 128, device=DEV).to(q.dtype)
+            lka.gqa_attn(q[:2].contiguous(), kk, kk, torch.full((2,), 60000, dtype=torch.int32, device=DEV))
+        assert lka.workspaces.get(256, q.device) is not before
+        assert lka.device_status() == BAD_LENGTH
+        lka.clear_status()
+        assert lka.device_status() == 0
