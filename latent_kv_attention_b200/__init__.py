@@ -151,24 +151,33 @@ class _Workspaces:
 
     The first 256 bytes of a workspace hold the library's sticky status word,
     which a larger workspace takes over from the one it replaces; the rest is
-    scratch that the kernels overwrite on every call."""
+    scratch that the kernels overwrite on every call.
+
+    A graph keeps the address of the workspace that a captured call was given:
+    that one is never freed."""
 
     def __init__(self):
         self._ws = {}
+        self._in_graphs = {}  # by address
         self._lock = threading.Lock()
 
     def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
         s = torch.cuda.current_stream(device) if stream is None else stream
         key = (device.index if device.index is not None else torch.cuda.current_device(), s.cuda_stream)
         nbytes = max(int(nbytes), 256)
+        capturing = device.type == "cuda" and torch.cuda.is_current_stream_capturing()
         with self._lock:
             t = self._ws.get(key)
-            if t is None or t.numel() < nbytes:
-                old, t = t, torch.zeros(nbytes + (1 << 20), dtype=torch.uint8, device=device)
-                # (a copy that a capture recorded would bring the old flags back with every replay)
-                if old is not None and not (t.is_cuda and torch.cuda.is_current_stream_capturing()):
-                    t[:4].copy_(old[:4])
-                self._ws[key] = t
+            if t is not None and t.numel() >= nbytes:
+                if capturing:
+                    self._in_graphs[t.data_ptr()] = t
+                return t
+            old, t = t, torch.zeros(nbytes + (1 << 20), dtype=torch.uint8, device=device)
+            if old is not None and not capturing:  # (a recorded copy would bring the old flags back with every replay)
+                t[:4].copy_(old[:4])
+            self._ws[key] = t
+            if capturing:
+                self._in_graphs[t.data_ptr()] = t
             return t
 
 

@@ -120,3 +120,31 @@ def test_status_outlives_the_growth_of_a_workspace(later):
         assert lka.device_status() == BAD_LENGTH
         lka.clear_status()
         assert lka.device_status() == 0
+
+
+def gqa_args(n, g):
+    """A gqa_attn call over n keys whose splits need a workspace of about 10 n bytes."""
+    q, k = randn(g, 2, 32, 1, 128), randn(g, 2, 8, n, 128)
+    return q, k, k, torch.full((2,), n, dtype=torch.int32, device=DEV)
+
+
+def test_a_captured_workspace_outlives_a_larger_one():
+    """A graph keeps the address of the workspace that its stream had: it stays the graph's when a later eager call on
+    the stream gets a larger one, and a replay writes to nothing else."""
+    g = gen(6)
+    s = torch.cuda.Stream()
+    args, larger = gqa_args(60000, g), gqa_args(240000, g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        want = lka.gqa_attn(*args).clone()
+        size = lka.workspaces.get(256, args[0].device).numel()
+    with torch.cuda.graph(graph, stream=s):
+        out = lka.gqa_attn(*args)
+    with torch.cuda.stream(s):
+        lka.gqa_attn(*larger)
+        assert lka.workspaces.get(256, args[0].device).numel() > size
+        others = [torch.full((size,), 5, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all((t == 5).all() for t in others)
