@@ -154,7 +154,9 @@ class _Workspaces:
     scratch that the kernels overwrite on every call.
 
     A graph keeps the address of the workspace that a captured call was given:
-    that one is never freed."""
+    that one is never freed.  Where the stream's is too small, a captured call
+    gets memory of the graph's own, zeroed by the graph and unknown to later
+    calls (whose flags, then, are not in any workspace of the stream)."""
 
     def __init__(self):
         self._ws = {}
@@ -172,12 +174,14 @@ class _Workspaces:
                 if capturing:
                     self._in_graphs[t.data_ptr()] = t
                 return t
+            if capturing:
+                t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                t[:256].zero_()
+                return t
             old, t = t, torch.zeros(nbytes + (1 << 20), dtype=torch.uint8, device=device)
-            if old is not None and not capturing:  # (a recorded copy would bring the old flags back with every replay)
+            if old is not None:
                 t[:4].copy_(old[:4])
             self._ws[key] = t
-            if capturing:
-                self._in_graphs[t.data_ptr()] = t
             return t
 
 

@@ -128,6 +128,32 @@ def gqa_args(n, g):
     return q, k, k, torch.full((2,), n, dtype=torch.int32, device=DEV)
 
 
+def test_a_workspace_of_a_capture_is_no_eager_call_s():
+    """A capture that needs a larger workspace than its stream has takes one of its graph's memory, whose zeros come with
+    the replay: an eager call on the stream must not find it."""
+    g = gen(5)
+    args = gqa_args(60000, g)
+    case = prefix_case((80, 8, 8, 1, 64, 300, 300, True, "bf16", 0), 2)[:6]
+    want, want_lse = (x.clone() for x in lka.gqa_attn_shared_prefix(*case, return_lse=True))
+    junk = torch.full((64 << 20,), 17, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    del junk
+    torch.cuda.empty_cache()  # what the graph allocates may hold anything
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = lka.gqa_attn(*args)
+    assert (args[0].device.index, s.cuda_stream) not in lka.workspaces._ws
+    with torch.cuda.stream(s):
+        got, lse = lka.gqa_attn_shared_prefix(*case, return_lse=True)
+        assert lka.device_status() == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, lka.gqa_attn(*args))
+
+
 def test_a_captured_workspace_outlives_a_larger_one():
     """A graph keeps the address of the workspace that its stream had: it stays the graph's when a later eager call on
     the stream gets a larger one, and a replay writes to nothing else."""
