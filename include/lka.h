@@ -497,6 +497,11 @@ LKA_API lka_status_t lka_kernel_timing_read(int *launches, double *total_ms);
  * for at most limit_us microseconds, then records LKA_ERR_TIMEOUT in ws's status word and exits.
  * Used to check the timeout path without hanging the GPU. */
 LKA_API lka_status_t lka_selftest_wait_timeout(void *ws, size_t ws_bytes, int limit_us, void *stream);
+/* Self-test of calls that fail half way, per host thread: of the launches behind the first kernel of the cache
+ * operators (e) that the calling thread makes from now on, the n-th asks for a block of 4096 threads, which the runtime
+ * refuses on the host: that call returns LKA_ERR_CUDA with the kernels before it enqueued.  0: none.  Returns how many
+ * such launches were still to come before a refused one. */
+LKA_API int lka_selftest_refuse_launch(int n);
 
 #ifdef __cplusplus
 }

@@ -102,6 +102,7 @@ SIGNATURES = {
     "lka_status_string": (ctypes.c_char_p, [_I]),
     "lka_set_split_tokens": (_I, [_I]),
     "lka_selftest_wait_timeout": (_I, [_P, _Z, _I, _P]),
+    "lka_selftest_refuse_launch": (_I, [_I]),
     "lka_kernel_timing": (_I, [_I]),
     "lka_kernel_timing_read": (_I, [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_double)]),
 }

@@ -391,7 +391,8 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cluster) != cudaSuccess) return LKA_ERR_CUDA;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cluster);
+    if (e != cudaSuccess) return call_status(e);
     MovePlan m;
     if (in_place) {
         // one block walks all rows of its slice: slices of 64 bytes (two sectors) give the parallelism
@@ -405,10 +406,10 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     m.slices = cdiv(p.row_bytes, m.slice);
     const dim3 grid((2 * m.slices + 1) * m.ranges, p.h_kv, p.B);
     TimedLaunch timer(st);
-    const cudaError_t e = in_place ? launch_pdl<evict_move_kernel<true>>(grid, kMoveThreads, 0, st, p, m)
-                                   : launch_pdl<evict_move_kernel<false>>(grid, kMoveThreads, 0, st, p, m);
+    e = in_place ? launch_pdl<evict_move_kernel<true>>(grid, kMoveThreads, 0, st, p, m)
+                 : launch_pdl<evict_move_kernel<false>>(grid, kMoveThreads, 0, st, p, m);
     timer.stop();
-    return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+    return call_status(e);
 }
 
 }  // namespace

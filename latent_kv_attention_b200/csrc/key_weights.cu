@@ -324,7 +324,7 @@ lka_status_t key_weights_run(const void* q, const void* k, const float* lse, con
         e = d == 64 ? launch_f32<64>(p, grid, st) : launch_f32<128>(p, grid, st);
     else
         e = d == 64 ? launch_mma<64>(p, grid, st) : d == 128 ? launch_mma<128>(p, grid, st) : launch_mma<256>(p, grid, st);
-    return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+    return call_status(e);
 }
 
 }  // namespace

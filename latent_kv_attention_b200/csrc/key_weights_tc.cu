@@ -298,7 +298,8 @@ static lka_status_t key_weights_tc_run(const KeyWeightParams& p, cudaStream_t st
     const uint64_t kd[3] = {(uint64_t)D, rows, slabs}, ks[2] = {row, row * rows};
     const uint32_t kb[3] = {64, (uint32_t)box_rows, 1};
     if (!make_tmap_nd(&tq, BF, p.q, 3, qd, qs, qb) || !make_tmap_nd(&tk, BF, p.k, 3, kd, ks, kb)) return LKA_ERR_CUDA;
-    if (allow_smem<key_weights_tc_kernel<D>>(C::SMEM) != cudaSuccess) return LKA_ERR_CUDA;
+    cudaError_t e = allow_smem<key_weights_tc_kernel<D>>(C::SMEM);
+    if (e != cudaSuccess) return call_status(e);
     const int key_tiles = cdiv(p.Lmax, kwt::TK);
     if (key_tiles > 65535) return LKA_ERR_UNSUPPORTED;
     // clusters share a key tile's queries while the key tiles alone leave SMs idle, and while every CTA keeps at
@@ -319,9 +320,9 @@ static lka_status_t key_weights_tc_run(const KeyWeightParams& p, cudaStream_t st
     cfg.attrs = at;
     cfg.numAttrs = 1;
     TimedLaunch timer(st);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<D>, tq, tk, p, cluster, box_rows);
+    e = cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<D>, tq, tk, p, cluster, box_rows);
     timer.stop();
-    return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+    return call_status(e);
 }
 
 lka_status_t key_weights_tc(const KeyWeightParams& p, int d, cudaStream_t st) {

@@ -1,11 +1,24 @@
-// launch_util.h -- host-side launch helper of the cache operators.
+// launch_util.h -- host-side launch helpers of the cache operators.
 #pragma once
 
 #include <cuda_runtime.h>
 
 #include <atomic>
 
+#include "../../include/lka.h"
+
 namespace lka {
+
+// The status of a call whose launches ended with `e`.  The runtime keeps a refused launch's error for whoever asks next:
+// it is taken here, so that the next call does not find it after a launch of its own.
+inline lka_status_t call_status(cudaError_t e) {
+    if (e == cudaSuccess) return LKA_OK;
+    cudaGetLastError();
+    return LKA_ERR_CUDA;
+}
+
+// Test hook, per host thread: the launches by launch_pdl until one is made that the runtime refuses (0: none is).
+inline thread_local int t_refused_launch = 0;
 
 // Allows a kernel `bytes` of dynamic shared memory, once per device (always the same bytes for one kernel).
 template <auto KERN>
@@ -29,6 +42,7 @@ cudaError_t launch_pdl(dim3 grid, int block, int smem, cudaStream_t st, const Ar
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
+    if (t_refused_launch > 0 && --t_refused_launch == 0) cfg.blockDim = dim3(4096);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];

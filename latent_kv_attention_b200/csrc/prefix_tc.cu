@@ -404,13 +404,14 @@ static lka_status_t prefix_tc_run(const PrefixParams& p, cudaStream_t st) {
     if (!make_tmap_nd(&tq, BF, p.q, 4, qd, qs, qb) || !make_tmap_nd(&tk, BF, p.kp, 3, kd, ks, kb) ||
         !make_tmap_nd(&tv, BF, p.vp, 3, kd, ks, kb))
         return LKA_ERR_CUDA;
-    if (allow_smem<prefix_tc_kernel<D>>(C::SMEM) != cudaSuccess) return LKA_ERR_CUDA;
+    const cudaError_t e = allow_smem<prefix_tc_kernel<D>>(C::SMEM);
+    if (e != cudaSuccess) return call_status(e);
     const long long n = (long long)cdiv(g.n_tiles, 2) * p.n_pre * p.h_kv;
     if (n >= (1ll << 31)) return LKA_ERR_UNSUPPORTED;
     TimedLaunch timer(st);
     prefix_tc_kernel<D><<<(unsigned)n, ptc::NT, C::SMEM, st>>>(tq, tk, tv, p, g);
     timer.stop();
-    return cudaPeekAtLastError() == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+    return call_status(cudaPeekAtLastError());
 }
 
 lka_status_t prefix_tc(const PrefixParams& p, int d, cudaStream_t st) {

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "launch_util.h"
 
 namespace lka {
 
@@ -378,8 +379,6 @@ cudaError_t rope_launch(RopeParams& p, bool inter, cudaStream_t st) {
     return cudaPeekAtLastError();
 }
 
-lka_status_t launch_status(cudaError_t e) { return e == cudaSuccess ? LKA_OK : LKA_ERR_CUDA; }
-
 bool elem_aligned(const void* ptr, int bytes) { return ptr && (reinterpret_cast<uintptr_t>(ptr) % bytes) == 0; }
 
 // What every form checks of the sizes: rotated width d_rot of heads of d values.
@@ -460,9 +459,9 @@ lka_status_t append_run(const void* q, const void* k, const void* v, const int64
     p.sign = 1.f;
     const cudaStream_t st = (cudaStream_t)stream;
     const bool inter = interleaved != 0;
-    if (c.fp8) return launch_status(rope_launch<__nv_bfloat16, __nv_fp8_e4m3>(p, inter, st));
-    if (dtype == LKA_BF16) return launch_status(rope_launch<__nv_bfloat16, __nv_bfloat16>(p, inter, st));
-    return launch_status(rope_launch<float, float>(p, inter, st));
+    if (c.fp8) return call_status(rope_launch<__nv_bfloat16, __nv_fp8_e4m3>(p, inter, st));
+    if (dtype == LKA_BF16) return call_status(rope_launch<__nv_bfloat16, __nv_bfloat16>(p, inter, st));
+    return call_status(rope_launch<float, float>(p, inter, st));
 }
 
 bool rope_pages_ok(const int32_t* table, int B, int page_size, int max_pages, int num_pages) {
@@ -503,8 +502,8 @@ lka_status_t rope_apply(const void* x, const int64_t* x_strides, const int32_t* 
     p.amplitude = amplitude;
     p.sign = backward ? -1.f : 1.f;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == LKA_BF16) return launch_status(rope_launch<__nv_bfloat16, __nv_bfloat16>(p, interleaved != 0, st));
-    return launch_status(rope_launch<float, float>(p, interleaved != 0, st));
+    if (dtype == LKA_BF16) return call_status(rope_launch<__nv_bfloat16, __nv_bfloat16>(p, interleaved != 0, st));
+    return call_status(rope_launch<float, float>(p, interleaved != 0, st));
 }
 
 lka_status_t gqa_rope_append(const void* q, const void* k, const void* v, const int64_t* strides,

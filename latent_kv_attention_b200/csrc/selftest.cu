@@ -1,8 +1,10 @@
 // selftest.cu -- exercises the bounded mbarrier wait used by every kernel:
 // one CTA waits on a barrier that nobody arrives at and must give up after the
-// given limit, recording LKA_ERR_TIMEOUT in the workspace status word.
+// given limit, recording LKA_ERR_TIMEOUT in the workspace status word.  And a
+// hook that makes a launch of a later call fail on the host.
 #include "common.cuh"
 #include "host_util.h"
+#include "launch_util.h"
 
 namespace lka {
 
@@ -25,4 +27,10 @@ extern "C" lka_status_t lka_selftest_wait_timeout(void* ws, size_t ws_bytes, int
     lka::wait_timeout_kernel<<<1, 32, 0, (cudaStream_t)stream>>>(static_cast<uint32_t*>(ws),
                                                                   (uint64_t)limit_us * 1000ull);
     return cudaPeekAtLastError() == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+}
+
+extern "C" int lka_selftest_refuse_launch(int n) {
+    const int before = lka::t_refused_launch;
+    lka::t_refused_launch = n > 0 ? n : 0;
+    return before;
 }

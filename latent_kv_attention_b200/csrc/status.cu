@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "launch_util.h"
 
 namespace lka {
 
@@ -41,5 +42,5 @@ extern "C" void* lka_captured_header(void) {
 extern "C" lka_status_t lka_add_status(void* to, const void* ws, void* stream) {
     if (!to || !ws || !lka::aligned16(to) || !lka::aligned16(ws)) return LKA_ERR_INVALID_ARG;
     lka::add_status_kernel<<<1, 1, 0, (cudaStream_t)stream>>>(static_cast<uint32_t*>(to), static_cast<const uint32_t*>(ws));
-    return cudaPeekAtLastError() == cudaSuccess ? LKA_OK : LKA_ERR_CUDA;
+    return lka::call_status(cudaPeekAtLastError());
 }

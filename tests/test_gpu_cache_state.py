@@ -174,3 +174,27 @@ def test_a_captured_workspace_outlives_a_larger_one():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
         assert all((t == 5).all() for t in others)
+
+
+def refused(n, call):
+    """The call fails at the n-th of its launches behind the first kernel, on the host."""
+    assert lka.library().lka_selftest_refuse_launch(n) == 0
+    with pytest.raises(lka.LkaError):
+        call()
+    assert lka.library().lka_selftest_refuse_launch(0) == 0
+
+
+@pytest.mark.parametrize("what", ["evict", "fp32 prefix"])
+def test_a_call_after_a_failed_one(what):
+    """A call that failed leaves no error behind for the next."""
+    g = gen(7)
+    if what == "evict":
+        k, w = randn(g, 2, 3, 400, 64), torch.rand(2, 3, 400, generator=g, device=DEV)
+        lens = torch.full((2,), 400, dtype=torch.int32, device=DEV)
+        call = lambda: lka.gqa_evict(k, k, w, lens, 50)  # noqa: E731
+    else:
+        case = prefix_case((5, 4, 2, 1, 64, 300, 30, True, "fp32", 0), 3)[:6]
+        call = lambda: lka.gqa_attn_shared_prefix(*case, return_lse=True)  # noqa: E731
+    want = [x.clone() for x in call()]
+    refused(1, call)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
