@@ -1077,7 +1077,10 @@ lka_status_t prefix_run(PrefixParams& p, int d, float scale, lka_dtype_t dtype, 
         e = d == 64 ? run_f32<64>(p, pl, st) : run_f32<128>(p, pl, st);
     else
         e = d == 64 ? run_bf16<64>(p, pl, st) : d == 128 ? run_bf16<128>(p, pl, st) : run_bf16<256>(p, pl, st);
-    return call_status(e);
+    const lka_status_t done = call_status(e);
+    // without a merge the suffix kernel's items stay counted, and a later call would skip as many
+    if (done != LKA_OK && cudaMemsetAsync(p.next_item, 0, sizeof(int), st) != cudaSuccess) cudaGetLastError();
+    return done;
 }
 
 bool prefix_pages_ok(int page_size, int max_prefix_pages, int max_pages, int num_pages) {

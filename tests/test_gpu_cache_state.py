@@ -198,3 +198,20 @@ def test_a_call_after_a_failed_one(what):
     want = [x.clone() for x in call()]
     refused(1, call)
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+@pytest.mark.parametrize("B,n", [(80, 1), (80, 2), (1, 1)])
+def test_a_shared_prefix_after_a_failed_one(B, n):
+    """A call whose merge (or suffix kernel) was refused leaves the counter of its work items as the next call expects it.
+    80 x 8 suffix items are more than the blocks that take them; one sequence of 8 x 2 heads takes its prefix in items."""
+    shape = (B, 16 if B == 1 else 8, 8, 1, 64, 4000 if B == 1 else 300, 300, True, "bf16", 0)
+    calls = [lambda case=prefix_case(shape, seed)[:6]: lka.gqa_attn_shared_prefix(*case, return_lse=True) for seed in (2, 3)]
+    prev = lka.set_split_tokens(64 if B == 1 else 0)
+    try:
+        want = [x.clone() for x in calls[1]()]
+        calls[0]()  # other partial results in the workspace
+        refused(n, calls[0])
+        assert all(torch.equal(a, b) for a, b in zip(calls[1](), want))
+    finally:
+        lka.set_split_tokens(prev)
+    assert lka.device_status() == 0
