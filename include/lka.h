@@ -488,7 +488,8 @@ LKA_API const char *lka_status_string(lka_status_t status);
 LKA_API int lka_set_split_tokens(int tokens);
 /* Timing hook for benchmarks, per host thread: lka_kernel_timing(1) discards the calling thread's earlier
  * records and starts recording a pair of CUDA events around the main (dominant) kernel of every later
- * entry-point call made from that thread, on that call's stream; lka_kernel_timing(0) stops recording.
+ * entry-point call made from that thread (of gqa_evict: its two kernels), on that call's stream;
+ * lka_kernel_timing(0) stops recording.
  * lka_kernel_timing_read waits for the calling thread's recorded events and returns the number of timed
  * launches and their summed duration in milliseconds.  Calls from other threads are never timed by it. */
 LKA_API lka_status_t lka_kernel_timing(int enable);

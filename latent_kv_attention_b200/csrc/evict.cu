@@ -391,6 +391,7 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    TimedLaunch timer(st);  // of both kernels: which is the longer depends on the shape
     cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cluster);
     if (e != cudaSuccess) return call_status(e);
     MovePlan m;
@@ -405,7 +406,6 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     }
     m.slices = cdiv(p.row_bytes, m.slice);
     const dim3 grid((2 * m.slices + 1) * m.ranges, p.h_kv, p.B);
-    TimedLaunch timer(st);
     e = in_place ? launch_pdl<evict_move_kernel<true>>(grid, kMoveThreads, 0, st, p, m)
                  : launch_pdl<evict_move_kernel<false>>(grid, kMoveThreads, 0, st, p, m);
     timer.stop();

@@ -976,7 +976,9 @@ cudaError_t launch_stream(const PrefixParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int blocks = (int)std::min<long long>(n, (long long)sm_count() * C::BLOCKS);
     if (p.do_prefix) {  // the call's first kernel
+        TimedLaunch timer(st);
         prefix_stream_kernel<D><<<blocks, 160, C::SMEM, st>>>(kp, vp, k, v, p, (int)n, box_rows);
+        timer.stop();
         return cudaPeekAtLastError();
     }
     return launch_pdl<prefix_stream_kernel<D>>(dim3(blocks), 160, C::SMEM, st, kp, vp, k, v, p, (int)n, box_rows);
