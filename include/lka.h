@@ -349,7 +349,8 @@ LKA_API lka_status_t rope_apply(const void *x, const int64_t *x_strides, const i
 
 /* Rotation of a step's queries and keys and the write of its keys and values into the cache.
  *   q [B,h_q,s_q,d_h], k, v [B,h_kv,s_q,d_h] through strides (host array of 9: q, k, v x batch, head, token)
- *   q_out [B,h_q,s_q,d_h] contiguous, q itself or apart from q, k, v; caches as in (a), (a') and (a'')
+ *   q_out [B,h_q,s_q,d_h] contiguous, q itself or apart from q, k, v; caches as in (a), (a') and (a''), apart from
+ *   one another and from all these
  * cache_lens[b] = L_b counts the cached tokens INCLUDING the s_q new ones: token t goes to row L_b - s_q + t.
  * positions [B,s_q] int32 or NULL (then the row is the position; a cache that has evicted keys passes the true
  * positions).  Tokens with L_b - s_q + t < 0 are padding: nothing is written for them and their q_out rows are 0

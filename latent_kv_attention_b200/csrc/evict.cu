@@ -330,11 +330,6 @@ __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 4 : 7) evict_move_ker
     }
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
 lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes, void* ws, void* stream) {
     if (p.B < 0 || p.h_kv < 1 || d < 1 || p.Lmax < 1 || p.Lout < 1 || p.budget < 1 || p.sinks < 0 || p.recent < 0)
         return LKA_ERR_INVALID_ARG;

@@ -421,6 +421,12 @@ lka_status_t append_run(const void* q, const void* k, const void* v, const int64
     if (c.fp8 && (!elem_aligned(c.k_scale, 4) || !elem_aligned(c.v_scale, 4))) return LKA_ERR_INVALID_ARG;
     if (!ws || ws_bytes < kWsHeaderBytes) return LKA_ERR_WORKSPACE;
     if (!aligned16(ws)) return LKA_ERR_INVALID_ARG;
+    // the caches and the rotated queries lie apart (the latent cache is one, its keys behind its values in every row)
+    const size_t cache_bytes = (size_t)(c.table ? c.num_pages : B) * c.slab * cb, q_bytes = (size_t)B * h_q * s * d * eb;
+    const bool one_cache = c.k_head == 0;
+    if (overlap(q_out, q_bytes, c.vc, cache_bytes) ||
+        (!one_cache && (overlap(q_out, q_bytes, c.kc, cache_bytes) || overlap(c.kc, cache_bytes, c.vc, cache_bytes))))
+        return LKA_ERR_INVALID_ARG;
     RopeParams p{};
     p.q = q;
     p.k = k;

@@ -1,0 +1,62 @@
+"""Operands of the cache operators that share memory where they must not (CPU only): refused on the host before anything
+is enqueued.  The addresses are never read."""
+import ctypes
+
+import pytest
+
+import latent_kv_attention_b200 as lka
+from latent_kv_attention_b200 import build
+
+P = ctypes.c_void_p
+INVALID, WORKSPACE = 1, 3
+Q, K, V, QO, KC, VC, LENS, FREQ, TABLE, SCALE, WS = (P((i + 1) << 24) for i in range(11))
+ST = (ctypes.c_int64 * 9)(*([64] * 9))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return lka.library()
+
+
+def at(p, off):
+    return P(p.value + off)
+
+
+def gqa(lib, q_out=QO, kc=KC, vc=VC, ws=WS):
+    """Caches of 3 x 2 x 32 rows of 64 bf16 values: 24,576 bytes; queries of 3 x 8 x 1 rows: 3072 bytes."""
+    return lib.gqa_rope_append(Q, K, V, ST, LENS, None, FREQ, q_out, kc, vc, 3, 8, 2, 1, 64, 64, 32, 0, 1.0, 0, ws, 256, None)
+
+
+def paged(lib, q_out=QO, kc=KC, vc=VC, ws=WS):
+    """Pools of 5 x 2 x 16 rows of 64 bf16 values: 20,480 bytes."""
+    return lib.gqa_rope_append_paged(Q, K, V, ST, TABLE, LENS, None, FREQ, q_out, kc, vc, 3, 8, 2, 1, 64, 64, 16, 2, 5, 0, 1.0,
+                                     0, ws, 256, None)
+
+
+def fp8(lib, q_out=QO, kc=KC, vc=VC, ws=WS):
+    """Caches of 12,288 bytes."""
+    return lib.gqa_rope_append_fp8kv(Q, K, V, ST, SCALE, SCALE, LENS, None, FREQ, q_out, kc, vc, 3, 8, 2, 1, 64, 64, 32, 0, 1.0,
+                                     ws, 256, None)
+
+
+def latent(lib, q_out=QO, cache=KC, ws=WS):
+    """A cache of 3 x 32 rows of 512 + 64 bf16 values: 110,592 bytes."""
+    return lib.latent_rope_append(Q, K, V, ST, LENS, None, FREQ, q_out, cache, 3, 8, 1, 512, 64, 32, 0, 1.0, 0, ws, 256, None)
+
+
+@pytest.mark.parametrize("call,size", [(gqa, 24576), (paged, 20480), (fp8, 12288)])
+def test_append_refuses_overlapping_caches_and_queries(lib, call, size):
+    assert call(lib, vc=at(KC, size - 16)) == INVALID
+    assert call(lib, kc=at(VC, size - 16)) == INVALID
+    assert call(lib, q_out=KC) == INVALID
+    assert call(lib, q_out=at(VC, size - 16)) == INVALID
+    assert call(lib, q_out=at(KC, -3072 + 16)) == INVALID
+    # next to each other is apart: what is missing then is the workspace
+    assert call(lib, vc=at(KC, size), q_out=at(KC, -3072), ws=None) == WORKSPACE
+
+
+def test_latent_append_refuses_queries_in_the_cache(lib):
+    assert latent(lib, q_out=at(KC, 110592 - 16)) == INVALID
+    assert latent(lib, q_out=at(KC, 1024)) == INVALID  # in its values
+    assert latent(lib, q_out=at(KC, 110592), ws=None) == WORKSPACE
