@@ -346,7 +346,8 @@ lka_status_t evict_run(EvictParams& p, int d, lka_dtype_t dtype, size_t ws_bytes
     if (p.new_lens == p.lens) return LKA_ERR_INVALID_ARG;
     const bool in_place = p.k == p.ko;
     if (p.table) {
-        if (p.ko == p.vo) return LKA_ERR_INVALID_ARG;
+        const size_t pool = (size_t)p.num_pages * p.h_kv * p.page_size * p.row_bytes;
+        if (overlap(p.ko, pool, p.vo, pool)) return LKA_ERR_INVALID_ARG;
     } else {
         const size_t rows_in = (size_t)p.B * p.h_kv * p.Lmax, rows_out = (size_t)p.B * p.h_kv * p.Lout;
         if (overlap(p.ko, rows_out * p.row_bytes, p.vo, rows_out * p.row_bytes)) return LKA_ERR_INVALID_ARG;

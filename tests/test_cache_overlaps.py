@@ -60,3 +60,14 @@ def test_latent_append_refuses_queries_in_the_cache(lib):
     assert latent(lib, q_out=at(KC, 110592 - 16)) == INVALID
     assert latent(lib, q_out=at(KC, 1024)) == INVALID  # in its values
     assert latent(lib, q_out=at(KC, 110592), ws=None) == WORKSPACE
+
+
+def test_paged_evict_refuses_overlapping_pools(lib):
+    """Pools of 5 x 2 x 16 rows of 64 bf16 values: 20,480 bytes."""
+    def call(vp, ws=WS):
+        return lib.gqa_evict_paged(KC, vp, P(20 << 24), TABLE, LENS, P(21 << 24), P(22 << 24), 1, 2, 64, 16, 2, 5, 8, 0, 0, 0, ws,
+                                   256, None)
+    assert call(KC) == INVALID
+    assert call(at(KC, 20480 - 16)) == INVALID
+    assert call(at(KC, -20480 + 16)) == INVALID
+    assert call(at(KC, 20480), ws=None) == WORKSPACE
