@@ -79,11 +79,21 @@ def _strided(t, name, dtype, device):
     return st
 
 
+def _distinct(shape, strides):
+    """Every element lies at an address of its own (each stride reaches past all that the smaller ones span)."""
+    span = 1
+    for st, n in sorted((st, n) for st, n in zip(strides, shape) if n > 1):
+        if st < span:
+            return False
+        span += (n - 1) * st
+    return True
+
+
 def _separate(out, os, x, xs, name, itself=False):
     """out (strides os) shares no memory with x (strides xs), or, if `itself`, is x."""
     a, b, e = out.data_ptr(), x.data_ptr(), x.element_size()
     if itself and a == b and all(n == 1 or i == j for n, i, j in zip(x.shape, os, xs)):
-        _require(all(st != 0 or n == 1 for n, st in zip(x.shape, xs)), f"in place needs {name} without repeated rows")
+        _require(_distinct(x.shape, xs), f"in place needs {name} without repeated or overlapping rows")
         return
     if out.numel() and x.numel():
         end_a, end_b = (at + e * (1 + sum((n - 1) * st for n, st in zip(t.shape, sts)))

@@ -3,9 +3,10 @@ is enqueued.  The addresses are never read."""
 import ctypes
 
 import pytest
+import torch
 
 import latent_kv_attention_b200 as lka
-from latent_kv_attention_b200 import build
+from latent_kv_attention_b200 import build, cache_ops
 
 P = ctypes.c_void_p
 INVALID, WORKSPACE = 1, 3
@@ -71,3 +72,17 @@ def test_paged_evict_refuses_overlapping_pools(lib):
     assert call(at(KC, 20480 - 16)) == INVALID
     assert call(at(KC, -20480 + 16)) == INVALID
     assert call(at(KC, 20480), ws=None) == WORKSPACE
+
+
+# ------------------------------------------------------------------ the binding
+@pytest.mark.parametrize("strides,ok", [((384, 128, 32, 1), True), ((384, 32, 96, 1), True), ((0, 128, 32, 1), False),
+                                        ((384, 128, 16, 1), False), ((384, 16, 32, 1), False), ((64, 128, 32, 1), False)])
+def test_in_place_needs_rows_of_their_own(strides, ok):
+    """A tensor [2, 3, 4, 32] of these strides, rotated in place: rows that are met twice would be turned twice."""
+    x = torch.empty(2048).as_strided((2, 3, 4, 32), strides)
+    assert ok == (len({int(i) for i in torch.arange(2048).as_strided(x.shape, strides).flatten()}) == x.numel())
+    if ok:
+        cache_ops._separate(x, strides, x, strides, "x", itself=True)
+    else:
+        with pytest.raises(ValueError):
+            cache_ops._separate(x, strides, x, strides, "x", itself=True)
