@@ -29,7 +29,7 @@ __device__ __forceinline__ void write_weight(const KeyWeightParams& p, size_t at
     p.w[at] = p.accumulate ? p.w[at] + v : v;
 }
 
-// The rows of the group a block walks: flat over (head, query) while a head has few queries; head by head, from
+// The rows of the group an fp32 block walks: flat over (head, query) while a head has few queries; head by head, from
 // the first query that sees the tile's first key, when it has many (a prompt's causal half is skipped).
 struct RowWalk {
     int segs, len, start;
@@ -45,8 +45,10 @@ __device__ __forceinline__ RowWalk row_walk(const KeyWeightParams& p, int j0, in
 // 32 j + 8 t .. + 7, the first four to k-step 2j, the last four to 2j + 1.
 // A decode step is bound by reading the keys: a warp walks `groups` groups of 16 keys and has the next group's loads
 // (4 KB at D = 128) under way while it works on this one.
+// Blocks per SM as many as the next tile's keys leave registers for (at d = 128 five: 116.7 us for 64 sequences of
+// 1024-8192 keys, caches out of L2; four, which the compiler takes to on its own, 122.9).
 template <int D>
-__global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightParams p) {
+__global__ void __launch_bounds__(128, D == 64 ? 8 : D == 128 ? 5 : 3) key_weights_mma_kernel(const KeyWeightParams p) {
     constexpr int NJ = D / 32;
     constexpr int QROW = D * 2 + 64;  // bytes; rows g and g + 1 fall in different halves of the banks
     extern __shared__ __align__(16) uint8_t smem[];
@@ -79,18 +81,10 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
     uint4 kr[2][NJ], kn[2][NJ];
     load_keys(block0, kr);
 
-    const RowWalk walk = row_walk(p, block0, L);
-    const int per_seg = cdiv(max(walk.len - walk.start, 0), chunk), n_chunks = walk.segs * per_seg;
+    const int n_rows = p.ratio * p.s, n_chunks = cdiv(n_rows, chunk);  // flat over (head, query): a head has few queries
     const size_t row0 = ((size_t)b * p.h_q + (size_t)kvh * p.ratio) * p.s;
-    auto chunk_at = [&](int c, int& first, int& n) {  // rows [first, first + n) of the group
-        const int seg = c / per_seg, r = walk.start + (c - seg * per_seg) * chunk;
-        first = seg * walk.len + r;
-        n = min(chunk, walk.len - r);
-    };
     auto stage = [&](int c) {
-        int first, n;
-        chunk_at(c, first, n);
-        const int buf = c & 1;
+        const int first = c * chunk, n = min(chunk, n_rows - first), buf = c & 1;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (row0 + first) * D;
         for (int i = threadIdx.x; i < chunk * (D / 8); i += 128) {
             const int r = i / (D / 8), ch = i % (D / 8);
@@ -104,7 +98,7 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
         cp_async_commit();
     };
     // Several tiles per block only where all rows are one chunk (kernel launch); otherwise one tile and all chunks.
-    if (n_chunks > 0) stage(0);
+    stage(0);
     for (int tile = 0; tile < n_tiles; ++tile) {
         const int j0 = block0 + tile * kTile;
         if (tile + 1 < n_tiles) load_keys(j0 + kTile, kn);
@@ -119,12 +113,11 @@ __global__ void __launch_bounds__(128) key_weights_mma_kernel(const KeyWeightPar
                 }
                 __syncthreads();
             }
-            int first, n;
-            chunk_at(c, first, n);
+            const int first = c * chunk, n = min(chunk, n_rows - first);
             const uint8_t* qb = qs + (size_t)(c & 1) * chunk * QROW;
             const float* lb = ls + (c & 1) * chunk;
-            // queries of this chunk that may not see every key of the tile need the mask
-            const bool masked = (p.causal && j0 + kTile - 1 > L - p.s + (p.s < kTile ? 0 : first % p.s)) || j0 + kTile > L;
+            // queries that may not see every key of the tile need the mask
+            const bool masked = (p.causal && j0 + kTile - 1 > L - p.s) || j0 + kTile > L;
 #pragma unroll 2
             for (int r0 = 0; r0 < n; r0 += 8) {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
