@@ -485,7 +485,8 @@ LKA_API lka_status_t lka_add_status(void *to, const void *ws, void *stream);
 LKA_API const char *lka_status_string(lka_status_t status);
 /* Split size (KV tokens per CTA) for the split-KV kernels of the calls made FROM THE CALLING HOST THREAD;
  * 0 restores the automatic choice.  A tuning and test knob: results do not depend on it beyond rounding,
- * and calls made from other threads keep their own setting (default 0).  Returns the thread's previous value. */
+ * and calls made from other threads keep their own setting (default 0).  More than 2^30 is taken as 2^30, negative
+ * as 0.  Returns the thread's previous value. */
 LKA_API int lka_set_split_tokens(int tokens);
 /* Timing hook for benchmarks, per host thread: lka_kernel_timing(1) discards the calling thread's earlier
  * records and starts recording a pair of CUDA events around the main (dominant) kernel of every later

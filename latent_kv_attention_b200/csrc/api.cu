@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <utility>
@@ -180,7 +181,7 @@ const char* lka_status_string(lka_status_t s) {
 
 int lka_set_split_tokens(int tokens) {
     const int prev = t_split_tokens;
-    t_split_tokens = tokens < 0 ? 0 : tokens;
+    t_split_tokens = tokens < 0 ? 0 : std::min(tokens, 1 << 30);  // no cache is longer; the plans round it up
     return prev;
 }
 
