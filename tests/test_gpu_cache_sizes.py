@@ -282,3 +282,31 @@ def test_pools_past_two_to_the_31_elements():
         moved = torch.gather(x, 2, at[..., None].expand(-1, -1, -1, d))
         assert torch.equal(from_pool(pool, table)[:, :, :700][live], moved[live])
         assert not pool[:-100].any()
+
+
+# ------------------------------------------------------------------ many query rows per head
+@pytest.mark.parametrize("split", [0, 128])
+@pytest.mark.parametrize("case", [
+    (2, 8, 2, 70, 128, 700, 90, True, "bf16", 0), (3, 4, 4, 200, 64, 333, 260, True, "bf16", 16), (1, 8, 1, 40, 256, 200, 64, True, "bf16", 0),
+    (2, 40, 2, 7, 128, 300, 50, False, "bf16", 64), (1, 4, 4, 129, 64, 1000, 129, True, "bf16", 0), (5, 64, 1, 2, 128, 450, 70, True, "bf16", 0),
+    (2, 4, 2, 50, 64, 300, 70, True, "fp32", 0), (1, 8, 2, 130, 128, 150, 140, True, "fp32", 8)],
+    ids=lambda c: f"{c[8]}B{c[0]}h{c[1]}kv{c[2]}s{c[3]}d{c[4]}p{c[9]}")
+def test_prompts_after_a_shared_prefix(case, split):
+    """More than 128 rows per sequence and KV head: row tiles of one sequence's, the last one started."""
+    test_shared_prefix_of_many_items(case, split)
+
+
+@pytest.mark.parametrize("B,h_q,h_kv,s,d,cap,causal,dtype", [(2, 64, 2, 30, 128, 300, True, "bf16"), (3, 32, 1, 63, 64, 130, False, "bf16"),
+                                                             (1, 16, 2, 33, 256, 200, True, "bf16"), (2, 64, 1, 63, 64, 100, True, "fp32"),
+                                                             (1, 24, 2, 150, 128, 190, True, "fp32"), (1, 128, 1, 64, 128, 500, True, "bf16")])
+def test_key_weights_of_many_rows(B, h_q, h_kv, s, d, cap, causal, dtype):
+    """Groups of more rows than are staged at a time, and heads that end inside a stage."""
+    g = gen(h_q + s)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k = randn(g, B, h_q, s, d, dtype=dt), randn(g, B, h_kv, cap, d, dtype=dt)
+    lens = torch.randint(s, cap + 1, (B,), generator=g, device=DEV).to(torch.int32)
+    lens[0] = cap
+    _, lse = lka.gqa_attn(q, k, k, lens, causal=causal, return_lse=True)
+    ref = want_weights(q, k, lse, lens, causal, d ** -0.5)
+    w = lka.gqa_key_weights(q, k, lse, lens, causal=causal)
+    assert ((w - ref).abs() <= 1e-5 * ref + 1e-30).all()
