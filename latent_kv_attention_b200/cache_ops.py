@@ -483,6 +483,13 @@ def gqa_key_weights_paged(q, k_pages, lse, block_table, cache_lens, weights=None
     return weights
 
 
+def _evict_counts(budget, sinks, recent):
+    """The three as the library takes them: no more sinks or recent keys than the budget (larger numbers mean the same,
+    and might not fit its integers)."""
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    return budget, min(sinks, max(budget, 0)), min(recent, max(budget, 0))
+
+
 def _evict_outputs(cache_lens, h_kv, budget):
     return torch.empty_like(cache_lens), cache_lens.new_empty((cache_lens.shape[0], h_kv, budget))
 
@@ -499,7 +506,7 @@ def gqa_evict(k, v, weights, cache_lens, budget: int, sinks: int = 0, recent: in
     dev, dt = k.device, k.dtype
     _require(k.is_cuda, "k must be a CUDA tensor")
     B, h_kv, Lmax, d = shape = k.shape
-    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    budget, sinks, recent = _evict_counts(budget, sinks, recent)
     if budget < 1 or sinks < 0 or recent < 0:
         raise ValueError("budget must be at least 1, sinks and recent at least 0")
     kp, vp = _dense(k, "k", dt, dev, shape), _dense(v, "v", dt, dev, shape)
@@ -536,7 +543,7 @@ def gqa_evict_paged(k_pages, v_pages, weights, block_table, cache_lens, budget: 
     table, max_pages = _table(block_table, B, dev)
     wp = _dense(weights, "weights", torch.float32, dev, (B, h_kv, max_pages * page_size))
     lens = _lens(cache_lens, B, dev)
-    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    budget, sinks, recent = _evict_counts(budget, sinks, recent)
     _require(1 <= budget <= max_pages * page_size and sinks >= 0 and recent >= 0,
              "budget must be between 1 and the table's capacity, sinks and recent at least 0")
     new_lens, kept = _evict_outputs(cache_lens, h_kv, budget)

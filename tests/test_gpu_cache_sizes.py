@@ -310,3 +310,17 @@ def test_key_weights_of_many_rows(B, h_q, h_kv, s, d, cap, causal, dtype):
     ref = want_weights(q, k, lse, lens, causal, d ** -0.5)
     w = lka.gqa_key_weights(q, k, lse, lens, causal=causal)
     assert ((w - ref).abs() <= 1e-5 * ref + 1e-30).all()
+
+
+@pytest.mark.parametrize("many", [50, 10 ** 6, 2 ** 31, 2 ** 32, 2 ** 32 + 3])
+def test_evict_counts_past_the_budget(many):
+    """More sinks or recent keys than the budget are the budget's worth of them, however many."""
+    g = gen(12)
+    k, w, lens = randn(g, 1, 2, 300, 16), torch.rand(1, 2, 300, generator=g, device=DEV), ints(300)
+    for kw in (dict(sinks=many), dict(recent=many), dict(sinks=20, recent=many)):
+        like = {n: min(x, 50) for n, x in kw.items()}
+        want, got = lka.gqa_evict(k, k, w, lens, 50, **like), lka.gqa_evict(k, k, w, lens, 50, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    pool, table = to_pool(k[:, :, :288].contiguous(), 16, g)
+    got = lka.gqa_evict_paged(pool, pool.clone(), w[:, :, :288].contiguous(), table, ints(288), 50, recent=many)[1]
+    assert (got == torch.arange(238, 288, device=DEV)).all()
