@@ -43,14 +43,6 @@ constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048, kKeep = 8;  // weights per thread that stay in registers
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ int2 cluster_load2(uint32_t addr, uint32_t rank) {
     uint32_t a;
     int2 v;

@@ -44,14 +44,6 @@ struct Cfg {
 };
 }  // namespace kwt
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
     uint32_t a;
     float v;

@@ -1,4 +1,4 @@
-// launch_util.h -- host-side launch helpers of the cache operators.
+// launch_util.h -- launch helpers of the cache operators, and what their kernels need of a launch's form.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -56,6 +56,15 @@ cudaError_t launch_pdl(dim3 grid, int block, int smem, cudaStream_t st, const Ar
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 #endif
 
 }  // namespace lka

@@ -39,12 +39,6 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two fp32 values as a bf16 pair (lo in the low half), rounded to nearest even.
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // The row of token `tok` of one head in a cache: contiguous (table == nullptr), or pages
 // [num_pages][heads][page_size].  An entry outside the pool raises kDevBadPage and gives -1.
 struct CacheRows {

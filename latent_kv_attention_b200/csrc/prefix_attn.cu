@@ -20,6 +20,7 @@
 #include "launch_util.h"
 #include "mma.cuh"
 #include "prefix_attn.h"
+#include "tc.cuh"
 
 namespace lka {
 
@@ -199,8 +200,8 @@ __device__ __forceinline__ void attend_tile(RowState<D>& st, const Q& q, const K
             for (int i = 0; i < 4; ++i) e[i] = fast_exp2(s[kg][n][i] - ms[i / 2]);
             st.l[0] += e[0] + e[1];
             st.l[1] += e[2] + e[3];
-            pa[2 * n] = bf16_pair(e[0], e[1]);
-            pa[2 * n + 1] = bf16_pair(e[2], e[3]);
+            pa[2 * n] = pack_bf16x2(e[0], e[1]);
+            pa[2 * n + 1] = pack_bf16x2(e[2], e[3]);
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -235,14 +236,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
-}
-
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
 }
 
 // Whether `pred` holds in any of the 128 consumer threads (named barrier 1 with an OR reduction).
@@ -349,8 +342,8 @@ __global__ void __launch_bounds__(160, StreamCfg<D>::BLOCKS)
                 if (r < C::TK) {
 #pragma unroll
                     for (int x = 0; x < C::NB; ++x) {
-                        tma_box(dst + x * C::BOX, mk, x * 64, y, z, fb);
-                        tma_box(dst + C::MAT + x * C::BOX, mv, x * 64, y, z, fb);
+                        tma_load_3d(dst + x * C::BOX, mk, x * 64, y, z, fb);
+                        tma_load_3d(dst + C::MAT + x * C::BOX, mv, x * 64, y, z, fb);
                     }
                 }
                 if (j + 1 < n_tiles) look_up(j + 1);
@@ -803,7 +796,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixParams p)
     if constexpr (sizeof(T) == 2) {
         uint32_t u[VPL / 2];
 #pragma unroll
-        for (int e = 0; e < VPL / 2; ++e) u[e] = bf16_pair(a[2 * e] * inv, a[2 * e + 1] * inv);
+        for (int e = 0; e < VPL / 2; ++e) u[e] = pack_bf16x2(a[2 * e] * inv, a[2 * e + 1] * inv);
         if constexpr (VPL == 2) *reinterpret_cast<uint32_t*>(out) = u[0];
         if constexpr (VPL == 4) *reinterpret_cast<uint2*>(out) = make_uint2(u[0], u[1]);
         if constexpr (VPL == 8) *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
