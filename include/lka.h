@@ -404,9 +404,10 @@ LKA_API lka_status_t latent_rope_append_fp8kv(const void *q_r, const void *c_kv,
  *   q, out [B,h_q,s_q,d_h]   k_prefix, v_prefix [h_kv,Lp,d_h]   k, v [B,h_kv,Lmax,d_h]   lse [B,h_q,s_q] or NULL
  *   prefix_len: device int32 [1] with 0 <= P <= Lp (clamped and reported), or NULL for P = Lp; Lp may be 0.
  * bf16 (d_h in {64, 128, 256}) or fp32 (d_h in {64, 128}).  The prefix is read once for the query rows of all
- * sequences together; softmax statistics and partial outputs are fp32.
+ * sequences together; softmax statistics and partial outputs are fp32, bf16 calls round the probabilities to bf16
+ * before their product with the values, as (a) does.  out may be q.  A NaN score makes NaN of its row's out and lse.
  * A non-finite value in a row that only some queries of the step see can reach the others, as in (a).
- * The workspace header also holds a work counter, 0 between calls.
+ * The workspace header also holds a work counter, 0 between calls (failed ones too).
  * Paged: one pool for prefix and suffixes; the prefix's pages are prefix_table [max_prefix_pages], a suffix starts
  * at row 0 of its own first page block_table[b][0].  Other arguments as in (a'). */
 LKA_API size_t gqa_attn_shared_prefix_workspace_size(int B, int h_q, int h_kv, int s_q, int d_h, int Lp, int Lmax,
@@ -431,7 +432,7 @@ LKA_API lka_status_t gqa_attn_shared_prefix_paged(const void *q, const void *k_p
  *                       exp(scale <q, k_j> - lse)
  *   q [B,h_q,s_q,d_h]  k [B,h_kv,Lmax,d_h] (or pages)  lse [B,h_q,s_q] as gqa_attn returned it
  *   weights [B,h_kv,Lmax] fp32: accumulate == 0 writes them (0 at j >= L_b), otherwise adds (j >= L_b untouched).
- * Rows with lse = -inf (no visible key) add nothing.  Deterministic (no atomics).  Types, lengths, masks and pages
+ * Rows with lse = -inf (no visible key) add nothing, whatever their queries hold.  Deterministic (no atomics).  Types, lengths, masks and pages
  * as in (a) and (a').  The workspace is only the status header (256 bytes). */
 LKA_API lka_status_t gqa_key_weights(const void *q, const void *k, const float *lse, const int32_t *cache_lens,
                                      float *weights, int B, int h_q, int h_kv, int s_q, int d_h, int Lmax, int causal,

@@ -7,7 +7,7 @@ operands may be strided views whose last dimension is contiguous (a projection's
 caches, pools and everything else is contiguous.
 
 Calls captured into a CUDA graph get scratch of their own from the graph's memory, so graphs that hold the same call
-can replay at the same time.
+can replay at the same time; their flags go to one header per device that device_status reads too.
 """
 from __future__ import annotations
 
@@ -170,7 +170,9 @@ def rope_inv_freq(d_rot: int, base: float = 10000.0, scaling: str | None = None,
       "ntk"     base times factor^(d_rot / (d_rot - 2)): the slowest pair is interpolated, the fastest kept
       "bands"   by the turns r = original_length * theta / 2 pi a pair makes over the trained length: r < low is
                 interpolated, r > high kept, linear in r between (default high 4: Llama-3.1)
-      "yarn"    the same with high 32, and amplitude 0.1 ln(factor) + 1 (Peng et al. 2023)
+      "yarn"    the same with high 32, and amplitude 0.1 ln(factor) + 1 (Peng et al. 2023, whose ramp is linear in the
+                turns; code that ramps over the pair index between the two borders gives the pairs there other
+                frequencies: take the one a checkpoint was trained with)
     """
     _require(d_rot >= 2 and d_rot % 2 == 0, "d_rot must be even")
     _require(base > 0 and factor > 0, "base and factor must be positive")

@@ -12,10 +12,10 @@
 //
 // Bound: 16,384 exponentials per tile are 1024 cycles of the special-function unit (16 per
 // cycle and SM) against 520 of the tensor pipe at d = 128.  Measured after a causal prompt of
-// 4096 tokens, 32 / 8 heads of 128 (16,896 tiles): 97 us, the unit about 0.7 busy.  The same in
-// one CTA per SM with four groups and one issuing thread 101 us (that thread's 1400 cycles per
-// tile), with three issuing threads 102-106; a quarter or three eighths of the exponentials as
-// polynomials on the FMA pipe 100-112 in every layout.
+// 4096 tokens, 32 / 8 heads of 128 (16,896 tiles): 106-107 us among other calls (97 at best), the
+// unit about 0.7 busy.  Beside the best figure: one CTA per SM with four groups and one issuing
+// thread 101 us (that thread's 1400 cycles per tile), with three issuing threads 102-106; a quarter
+// or three eighths of the exponentials as polynomials on the FMA pipe 100-112 in every layout.
 #include <math.h>
 
 #include <algorithm>
