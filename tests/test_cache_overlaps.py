@@ -25,19 +25,19 @@ def at(p, off):
 
 
 def gqa(lib, q_out=QO, kc=KC, vc=VC, ws=WS):
-    """Caches of 3 x 2 x 32 rows of 64 bf16 values: 24,576 bytes; queries of 3 x 8 x 1 rows: 3072 bytes."""
-    return lib.gqa_rope_append(Q, K, V, ST, LENS, None, FREQ, q_out, kc, vc, 3, 8, 2, 1, 64, 64, 32, 0, 1.0, 0, ws, 256, None)
+    """Caches of 3 x 2 x 32 rows of 64 bf16 values: 24,576 bytes; queries of 3 x 4 x 1 rows: 1536 bytes."""
+    return lib.gqa_rope_append(Q, K, V, ST, LENS, None, FREQ, q_out, kc, vc, 3, 4, 2, 1, 64, 64, 32, 0, 1.0, 0, ws, 256, None)
 
 
 def paged(lib, q_out=QO, kc=KC, vc=VC, ws=WS):
     """Pools of 5 x 2 x 16 rows of 64 bf16 values: 20,480 bytes."""
-    return lib.gqa_rope_append_paged(Q, K, V, ST, TABLE, LENS, None, FREQ, q_out, kc, vc, 3, 8, 2, 1, 64, 64, 16, 2, 5, 0, 1.0,
+    return lib.gqa_rope_append_paged(Q, K, V, ST, TABLE, LENS, None, FREQ, q_out, kc, vc, 3, 4, 2, 1, 64, 64, 16, 2, 5, 0, 1.0,
                                      0, ws, 256, None)
 
 
 def fp8(lib, q_out=QO, kc=KC, vc=VC, ws=WS):
     """Caches of 12,288 bytes."""
-    return lib.gqa_rope_append_fp8kv(Q, K, V, ST, SCALE, SCALE, LENS, None, FREQ, q_out, kc, vc, 3, 8, 2, 1, 64, 64, 32, 0, 1.0,
+    return lib.gqa_rope_append_fp8kv(Q, K, V, ST, SCALE, SCALE, LENS, None, FREQ, q_out, kc, vc, 3, 4, 2, 1, 64, 64, 32, 0, 1.0,
                                      ws, 256, None)
 
 
@@ -52,9 +52,9 @@ def test_append_refuses_overlapping_caches_and_queries(lib, call, size):
     assert call(lib, kc=at(VC, size - 16)) == INVALID
     assert call(lib, q_out=KC) == INVALID
     assert call(lib, q_out=at(VC, size - 16)) == INVALID
-    assert call(lib, q_out=at(KC, -3072 + 16)) == INVALID
+    assert call(lib, q_out=at(KC, -1536 + 16)) == INVALID
     # next to each other is apart: what is missing then is the workspace
-    assert call(lib, vc=at(KC, size), q_out=at(KC, -3072), ws=None) == WORKSPACE
+    assert call(lib, vc=at(KC, size), q_out=at(KC, -1536), ws=None) == WORKSPACE
 
 
 def test_latent_append_refuses_queries_in_the_cache(lib):
